@@ -59,7 +59,9 @@ typedef enum {
   BITNET_ERR_DTYPE = 4,     /* unknown bitnet_dtype / bitnet_act value                    */
   BITNET_ERR_WORKSPACE = 5, /* workspace missing or smaller than the *_workspace_bytes() */
   BITNET_ERR_CUDA = 6,      /* a CUDA call failed; see bitnet_last_error()               */
-  BITNET_ERR_TIMEOUT = 7    /* a kernel gave up a bounded wait (device status word)      */
+  BITNET_ERR_TIMEOUT = 7,   /* a kernel gave up a bounded wait (device status word)      */
+  BITNET_ERR_INDEX = 8      /* a length, page or slot on the device was out of range and was
+                               skipped (device status word)                               */
 } bitnet_status;
 
 typedef enum { BITNET_BF16 = 0, BITNET_F32 = 1 } bitnet_dtype;
@@ -311,9 +313,97 @@ bitnet_status bitnet_attention_decode(const float* q_rot, const void* k_cache, c
                                       int64_t Hq, int64_t Hkv, int64_t d, int64_t pos0, int64_t L_max, void* out,
                                       bitnet_dtype ot, void* ws, size_t ws_bytes, bitnet_stream s);
 
+/* ---- One serving step of many requests over a paged KV cache ------------------------------
+ * The same block for continuous batching: the tokens of a step belong to up to
+ * BITNET_MAX_REQUESTS requests, each with its own cached tokens, whose keys and values lie in
+ * pages of one pool:
+ *   k_pages, v_pages   bf16 [n_pages][Hkv][page_size][128]; page_size 16, 32, 64, 128 or 256
+ *   block_table        int32 [B][width]; entry j of request i is the page of its rows
+ *                      j page_size .. (j + 1) page_size - 1
+ *   slot               page * page_size + row of the page (the same row in every head)
+ * Lengths, tables, slots and page ids are device data that the host never reads, so a step can be
+ * captured into a graph and replayed.  A value out of range is never followed: the access is
+ * skipped and the device status word set to BITNET_ERR_INDEX.  (The BitNet pages have no
+ * counterpart: the arithmetic is that of the single-sequence entries above, over a paged cache.) */
+#define BITNET_MAX_REQUESTS 4096
+#define BITNET_MAX_STEP_TOKENS (1 << 22)
+
+/* Residual addition in front of bitnet_rmsnorm_quant_act:
+ *   r' = x + residual (one fp32 addition, rounded to the residual's type rt)   -> residual_out
+ *   (q, s_x, sum_q) = rmsnorm_quant_act(r', gain, eps), bit for bit
+ * x [T, K] (xt) is a sublayer's output, residual [T, K] (rt) the stream before it; both types are
+ * free.  residual_out may be the residual itself (in place); other overlaps are not allowed.
+ * Errors as bitnet_rmsnorm_quant_act. */
+bitnet_status bitnet_add_rmsnorm_quant_act(const void* x, bitnet_dtype xt, const void* residual, bitnet_dtype rt,
+                                           const float* gain, float eps, int64_t T, int64_t K, void* residual_out,
+                                           int8_t* q, float* s_x, int32_t* sum_q, bitnet_stream s);
+
+/* The plan of a step: request i has ctx_lens[i] cached tokens and brings new_lens[i] new ones
+ * (0 allowed).
+ *   cu_new [B + 1]    tokens of the step before request i (cu_new[B]: all of them)
+ *   kv_lens [B]       ctx_lens[i] + new_lens[i]
+ *   block_table       request i's new pages, ceil(kv / page_size) - ceil(ctx / page_size) of them, are
+ *                     written behind its old ones, taken from the end of the free list request
+ *                     by request: free_pages[n_free - 1], free_pages[n_free - 2], ...  Other
+ *                     entries are left as they were
+ *   n_free_out [1]    n_free less the pages taken
+ *   positions [T]     position of each of the step's tokens (0 behind the last one)
+ *   slots [T]         its slot (-1 behind the last one)
+ * All int32 on the device, 4-byte aligned; n_list is the allocated length of free_pages, n_free
+ * [1] how many of its entries are free.  The call takes pages but does not change the list: the
+ * caller's new count is n_free_out (which must not be n_free itself).  A calling program returns a
+ * finished request's pages by writing them behind the free ones.
+ * If the free pages do not suffice, n_free_out is negative (how many are missing), the entries
+ * and slots without a page are -1, and the step must not be run.  A request with a negative
+ * length, or whose tokens exceed width * page_size, gets no pages, its slots are -1 and its kv_len
+ * is its ctx_len (in range); if the new lengths add up to more than T, cu_new stops at T; both set
+ * BITNET_ERR_INDEX, as does an n_free outside [0, n_list].  T may exceed the tokens (padding of a
+ * fixed-size step).
+ * Errors: NULL, SHAPE (B > BITNET_MAX_REQUESTS, T > BITNET_MAX_STEP_TOKENS, page_size, or
+ * width * page_size beyond int32), ALIGN. */
+bitnet_status bitnet_paged_plan(const int32_t* new_lens, const int32_t* ctx_lens, int64_t B, int64_t page_size,
+                                int32_t* block_table, int64_t width, const int32_t* free_pages, int64_t n_list,
+                                const int32_t* n_free, int64_t T, int32_t* cu_new, int32_t* kv_lens,
+                                int32_t* positions, int32_t* slots, int32_t* n_free_out, bitnet_stream s);
+
+/* bitnet_rope_kv_append for tokens at any positions and slots: token t is rotated at positions[t],
+ * its rotated k and its v go to slot slots[t] of the pages.  q_rot is bf16 [T, Hq, 128] here
+ * (nearest even; what the paged attention multiplies).  Tokens with a negative slot are skipped:
+ * neither their q_rot nor the cache is written.  A slot of n_pages * page_size or more is skipped
+ * too and sets BITNET_ERR_INDEX.  The slots of a call must differ from one another.  The angle is
+ * p theta^(-2i/128) reduced to a turn in fp64, its sine and cosine fp32.  Errors: NULL, SHAPE (d != 128, Hq % Hkv,
+ * Hq > 1024, page_size, theta <= 0), ALIGN, DTYPE. */
+bitnet_status bitnet_rope_paged_append(const void* q, const void* k, const void* v, bitnet_dtype xt, int64_t T,
+                                       int64_t Hq, int64_t Hkv, int64_t d, const int32_t* positions,
+                                       const int32_t* slots, double theta, void* q_rot, void* k_pages, void* v_pages,
+                                       int64_t n_pages, int64_t page_size, bitnet_stream s);
+
+/* Workspace of bitnet_attention_paged on the current device, in bytes (0 if invalid); it does not
+ * depend on the lengths. */
+size_t bitnet_attention_paged_workspace_bytes(int64_t Hq, int64_t Hkv, int64_t max_new);
+
+/* Causal grouped-query attention of each request's new tokens (in the cache already) over its
+ * pages: token t' of request i, row cu_new[i] + t' of q_rot (bf16 [T, Hq, 128]), sees cache rows
+ * 0 .. kv_lens[i] - new_i + t', new_i = cu_new[i + 1] - cu_new[i]:
+ *   out[., h] = softmax(q_rot[., h] . k / sqrt(128)) v, key/value head h / (Hq / Hkv)
+ * out: bf16 or fp32 [T, Hq, 128].  max_new: no request has more new tokens (1 for a decode step).
+ * A token that sees no row (kv_lens[i] < new_i) gets zeros.  Rows of out outside the requests'
+ * tokens are left as they were; cache rows at and behind kv_lens[i] may hold anything.  A
+ * non-finite value in a visible row makes the outputs of that request and head undefined, of
+ * no other.  Scores, maxima, sums and outputs are held in fp32; equal calls give equal bits.  A request whose lengths do not
+ * fit the call (cu_new descending or beyond T, more than max_new tokens, kv_lens beyond the
+ * table) is skipped; a page id outside [0, n_pages) counts as a page of zeros; both set
+ * BITNET_ERR_INDEX.  Two calls that share a workspace must not run concurrently.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, WORKSPACE. */
+bitnet_status bitnet_attention_paged(const void* q_rot, const void* k_pages, const void* v_pages,
+                                     const int32_t* block_table, const int32_t* cu_new, const int32_t* kv_lens,
+                                     int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t d, int64_t n_pages,
+                                     int64_t page_size, int64_t width, int64_t max_new, void* out, bitnet_dtype ot,
+                                     void* ws, size_t ws_bytes, bitnet_stream s);
+
 /* Synchronises `s`, then reads and clears the device status word of the current
- * device: BITNET_OK, or BITNET_ERR_TIMEOUT if a kernel gave up a bounded wait since
- * the last read. */
+ * device: BITNET_OK, BITNET_ERR_TIMEOUT if a kernel gave up a bounded wait since the last
+ * read, or BITNET_ERR_INDEX if one skipped an index out of range (the later of the two). */
 bitnet_status bitnet_get_device_status(bitnet_stream s);
 
 /* Test and debugging aid (no counterpart on the pages): sets the limit of every bounded wait

@@ -17,6 +17,7 @@ __all__ = [
     "lib", "i2s_packed_bytes", "pack_i2s", "rmsnorm_quant_act", "bitlinear", "bitlinear_group", "bitlinear_gate_up_act",
     "ffn_workspace_bytes", "ffn_workspace_offsets", "ffn_block", "ffn_block_noalloc", "block_workspace_bytes", "block_workspace_offsets",
     "decoder_block", "device_status", "BitnetError",
+    "add_rmsnorm_quant_act", "paged_plan", "rope_paged_append", "attention_paged", "attention_paged_workspace_bytes",
     "BF16", "F32", "RELU2", "SILU",
 ]
 
@@ -27,7 +28,7 @@ BF16, F32 = 0, 1
 RELU2, SILU = 0, 1
 _STATUS = {0: "ok", 1: "null pointer", 2: "invalid shape", 3: "pointer not 16-byte aligned",
            4: "invalid dtype or activation", 5: "workspace missing or too small", 6: "CUDA error",
-           7: "kernel wait timed out"}
+           7: "kernel wait timed out", 8: "device-side length, page or slot out of range"}
 
 EXPORTS = [
     "bitnet_i2s_packed_bytes", "bitnet_pack_i2s", "bitnet_rmsnorm_quant_act", "bitnet_bitlinear",
@@ -35,6 +36,8 @@ EXPORTS = [
     "bitnet_ffn_block", "bitnet_ffn_block_noalloc_max_bytes", "bitnet_ffn_block_noalloc",
     "bitnet_block_workspace_bytes", "bitnet_block_workspace_offsets", "bitnet_decoder_block",
     "bitnet_get_device_status", "bitnet_status_string", "bitnet_last_error",
+    "bitnet_add_rmsnorm_quant_act", "bitnet_paged_plan", "bitnet_rope_paged_append",
+    "bitnet_attention_paged_workspace_bytes", "bitnet_attention_paged",
 ]
 
 
@@ -91,6 +94,14 @@ def lib() -> ctypes.CDLL:
         "bitnet_attention_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64, c_i64]),
         "bitnet_attention_decode": (c_i, [c_p, c_p, c_p, c_i64, c_i64, c_i64, c_i64, c_i64, c_i64, c_p, c_i, c_p, c_sz,
                                           c_p]),
+        "bitnet_add_rmsnorm_quant_act": (c_i, [c_p, c_i, c_p, c_i, c_p, c_f, c_i64, c_i64, c_p, c_p, c_p, c_p, c_p]),
+        "bitnet_paged_plan": (c_i, [c_p, c_p, c_i64, c_i64, c_p, c_i64, c_p, c_i64, c_p, c_i64, c_p, c_p, c_p, c_p, c_p,
+                                    c_p]),
+        "bitnet_rope_paged_append": (c_i, [c_p, c_p, c_p, c_i, c_i64, c_i64, c_i64, c_i64, c_p, c_p, ctypes.c_double,
+                                           c_p, c_p, c_p, c_i64, c_i64, c_p]),
+        "bitnet_attention_paged_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64]),
+        "bitnet_attention_paged": (c_i, [c_p, c_p, c_p, c_p, c_p, c_p, c_i64, c_i64, c_i64, c_i64, c_i64, c_i64, c_i64,
+                                         c_i64, c_i64, c_p, c_i, c_p, c_sz, c_p]),
         "bitnet_get_device_status": (c_i, [c_p]),
         "bitnet_debug_set_wait_limit": (c_i, [ctypes.c_longlong]),
         "bitnet_status_string": (ctypes.c_char_p, [c_i]),
@@ -394,6 +405,162 @@ def attention_decode(q_rot, k_cache, v_cache, pos0: int, out_dtype=torch.bfloat1
                                          _ptr(o), _dtype_code(o.dtype), _ptr(w), w.numel(), _stream(stream)),
            "attention_decode")
     return o
+
+
+# ------------------------------------------------------- a serving step over a paged KV cache
+
+_I32, _F32T, _BF16T = torch.int32, torch.float32, torch.bfloat16
+
+
+def _same_device(dev: torch.device, name: str, t: torch.Tensor, dtypes: tuple) -> None:
+    if not t.is_cuda or t.device != dev or not t.is_contiguous() or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be a contiguous tensor on {dev} of type {' or '.join(map(str, dtypes))}")
+
+
+def _current(t: torch.Tensor, name: str) -> torch.device:
+    """The device of a call's first tensor, which has to be the current one (the stream is its)."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    return t.device
+
+
+def add_rmsnorm_quant_act(x, residual, gain, eps: float = 1e-6, residual_out=None, out=None, stream=None):
+    """x and residual bf16/fp32 [T, K] -> (residual + x in residual's type, q int8 [T, K], s_x fp32 [T],
+    sum_q int32 [T]), the last three those of ``rmsnorm_quant_act`` of the first.  ``residual_out`` may be
+    ``residual`` itself."""
+    dev = _current(x, "x")
+    T, K = x.shape
+    _same_device(dev, "x", x, (_BF16T, _F32T))
+    _same_device(dev, "residual", residual, (_BF16T, _F32T))
+    if residual.shape != x.shape:
+        raise ValueError("residual must have the shape of x")
+    if gain is not None:
+        _same_device(dev, "gain", gain, (_F32T,))
+        if gain.numel() != K:
+            raise ValueError("gain must have K entries")
+    if residual_out is None:
+        residual_out = torch.empty_like(residual)
+    else:
+        _same_device(dev, "residual_out", residual_out, (residual.dtype,))
+        if residual_out.shape != x.shape:
+            raise ValueError("residual_out must have the shape of x")
+    if out is None:
+        out = (torch.empty(T, K, dtype=torch.int8, device=dev), torch.empty(T, dtype=_F32T, device=dev),
+               torch.empty(T, dtype=_I32, device=dev))
+    else:
+        for t, n, dt, nm in zip(out, (T * K, T, T), (torch.int8, _F32T, _I32), ("q", "s_x", "sum_q")):
+            _same_device(dev, nm, t, (dt,))
+            if t.numel() != n:
+                raise ValueError(f"{nm} must have {n} entries")
+    q, s, sq = out
+    _check(lib().bitnet_add_rmsnorm_quant_act(_ptr(x), _dtype_code(x.dtype), _ptr(residual), _dtype_code(residual.dtype),
+                                              _ptr(gain), eps, T, K, _ptr(residual_out), _ptr(q), _ptr(s), _ptr(sq),
+                                              _stream(stream)), "add_rmsnorm_quant_act")
+    return residual_out, q, s, sq
+
+
+def paged_plan(new_lens, ctx_lens, block_table, free_pages, n_free, page_size: int, T: int, out=None, stream=None):
+    """Plan of a step of T tokens (padding included) -> (cu_new [B + 1], kv_lens [B], positions [T], slots [T],
+    n_free_out [1]); the requests' new pages are written into ``block_table`` [B, width].  All int32."""
+    dev = _current(new_lens, "new_lens")
+    B, width = block_table.shape
+    for t, n, nm in ((new_lens, B, "new_lens"), (ctx_lens, B, "ctx_lens"), (block_table, B * width, "block_table"),
+                     (free_pages, free_pages.numel(), "free_pages"), (n_free, 1, "n_free")):
+        _same_device(dev, nm, t, (_I32,))
+        if t.numel() != n:
+            raise ValueError(f"{nm} must have {n} entries")
+    sizes = (B + 1, B, T, T, 1)
+    if T < 0:
+        raise BitnetError(2, "paged_plan")
+    if out is None:
+        # one allocation; every part starts on a 4-byte boundary, which is all the step's calls need
+        out = torch.empty(2 * B + 2 + 2 * T, dtype=_I32, device=dev).split_with_sizes(sizes)
+    else:
+        for t, n, nm in zip(out, sizes, ("cu_new", "kv_lens", "positions", "slots", "n_free_out")):
+            _same_device(dev, nm, t, (_I32,))
+            if t.numel() != n:
+                raise ValueError(f"{nm} must have {n} entries")
+    cu, kv, pos, slots, left = out
+    if left.data_ptr() == n_free.data_ptr():
+        raise ValueError("n_free_out must not be n_free")
+    _check(lib().bitnet_paged_plan(_ptr(new_lens), _ptr(ctx_lens), B, page_size, _ptr(block_table), width,
+                                   _ptr(free_pages), free_pages.numel(), _ptr(n_free), T, _ptr(cu), _ptr(kv), _ptr(pos),
+                                   _ptr(slots), _ptr(left), _stream(stream)), "paged_plan")
+    return cu, kv, pos, slots, left
+
+
+def _pages(dev, k_pages, v_pages, Hkv: int, d: int):
+    _same_device(dev, "k_pages", k_pages, (_BF16T,))
+    _same_device(dev, "v_pages", v_pages, (_BF16T,))
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[3] != d or k_pages.shape[1] != Hkv:
+        raise ValueError("k_pages and v_pages must be [n_pages, Hkv, page_size, d]")
+    return k_pages.shape[0], k_pages.shape[2]
+
+
+def rope_paged_append(q, k, v, positions, slots, theta: float, k_pages, v_pages, q_rot=None, stream=None) -> torch.Tensor:
+    """Rotate q [T, Hq, 128] and k [T, Hkv, 128] (bf16 or fp32) at positions [T]; write k (rotated) and v to slots [T]
+    of the bf16 pages [n_pages, Hkv, page_size, 128].  Returns q_rot (bf16 [T, Hq, 128]); tokens with a negative
+    slot are skipped."""
+    dev = _current(q, "q")
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    for t, nm in ((q, "q"), (k, "k"), (v, "v")):
+        _same_device(dev, nm, t, (_BF16T, _F32T))
+        if t.dtype != q.dtype:
+            raise ValueError("q, k and v must have one type")
+    if k.shape != (T, Hkv, d) or v.shape != k.shape:
+        raise ValueError("k and v must be [T, Hkv, d]")
+    for t, nm in ((positions, "positions"), (slots, "slots")):
+        _same_device(dev, nm, t, (_I32,))
+        if t.numel() != T:
+            raise ValueError(f"{nm} must have {T} entries")
+    n_pages, P = _pages(dev, k_pages, v_pages, Hkv, d)
+    if q_rot is None:
+        q_rot = torch.empty(T, Hq, d, dtype=_BF16T, device=dev)
+    else:
+        _same_device(dev, "q_rot", q_rot, (_BF16T,))
+        if q_rot.shape != q.shape:
+            raise ValueError("q_rot must have the shape of q")
+    _check(lib().bitnet_rope_paged_append(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q.dtype), T, Hq, Hkv, d, _ptr(positions),
+                                          _ptr(slots), float(theta), _ptr(q_rot), _ptr(k_pages), _ptr(v_pages), n_pages,
+                                          P, _stream(stream)), "rope_paged_append")
+    return q_rot
+
+
+def attention_paged_workspace_bytes(Hq: int, Hkv: int, max_new: int) -> int:
+    return int(lib().bitnet_attention_paged_workspace_bytes(Hq, Hkv, max_new))
+
+
+def attention_paged(q_rot, k_pages, v_pages, block_table, cu_new, kv_lens, max_new: int, out_dtype=torch.bfloat16,
+                    out=None, ws=None, stream=None) -> torch.Tensor:
+    """Causal GQA attention of q_rot (bf16 [T, Hq, 128]), the new tokens of B requests back to back (request i:
+    rows cu_new[i] .. cu_new[i + 1] - 1, at most max_new), over each request's pages.  Rows of ``out`` behind the
+    last request are left as they were."""
+    dev = _current(q_rot, "q_rot")
+    T, Hq, d = q_rot.shape
+    B, width = block_table.shape
+    _same_device(dev, "q_rot", q_rot, (_BF16T,))
+    Hkv = k_pages.shape[1]
+    n_pages, P = _pages(dev, k_pages, v_pages, Hkv, d)
+    for t, n, nm in ((block_table, B * width, "block_table"), (cu_new, B + 1, "cu_new"), (kv_lens, B, "kv_lens")):
+        _same_device(dev, nm, t, (_I32,))
+        if t.numel() != n:
+            raise ValueError(f"{nm} must have {n} entries")
+    if out is None:
+        out = torch.empty(T, Hq, d, dtype=out_dtype, device=dev)
+    else:
+        _same_device(dev, "out", out, (_BF16T, _F32T))
+        if out.shape != q_rot.shape:
+            raise ValueError("out must have the shape of q_rot")
+    if ws is None:
+        ws = torch.empty(max(attention_paged_workspace_bytes(Hq, Hkv, max_new), 16), dtype=torch.uint8, device=dev)
+    else:
+        _same_device(dev, "ws", ws, (torch.uint8,))
+    _check(lib().bitnet_attention_paged(_ptr(q_rot), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(cu_new),
+                                        _ptr(kv_lens), T, B, Hq, Hkv, d, n_pages, P, width, max_new, _ptr(out),
+                                        _dtype_code(out.dtype), _ptr(ws), ws.numel(), _stream(stream)),
+           "attention_paged")
+    return out
 
 
 def debug_set_wait_limit(cycles: int) -> None:

@@ -1,0 +1,492 @@
+// Causal grouped-query attention of each request's new tokens over its pages of the cache:
+//   out[t, h] = sum_l w_l v_l,  w = softmax over l of (q[t, h] . k_l) / sqrt(128),
+// l running over the request's rows 0 .. kv - new + t' (t' = the token's place among the
+// request's new tokens), query head h reading key/value head h / G, G = Hq / Hkv.  A row that
+// sees nothing is zero.
+//
+// Work is cut the same way for every size.  The query rows r = t' G + g of one request and one
+// key/value head (all of them read the same keys) form tiles of M rows; a tile's visible cache
+// rows form units of U rows.  All units of all tiles, in the order request, head, tile, unit, make
+// one line, and every CTA takes the same number of consecutive units.  So a long cache with one
+// query row, a ragged batch and a causal triangle are all spread evenly without the host knowing a
+// length.  A tile that lies in one CTA's share is written straight to the output; of the others
+// each CTA keeps (running maximum, sum, weighted values) in the workspace, at most two per CTA
+// (the tile that its share begins in and the one that it ends in), and a second launch joins
+// them in the order of the units.  The cut depends on the lengths and the GPU alone, so results
+// repeat bit for bit.
+#pragma once
+#include "common.cuh"
+#include "gemv.cuh"
+#include "paged.cuh"
+
+namespace bitnet {
+
+struct PagedArgs {
+  const __nv_bfloat16* q;        // [T][Hq][128]
+  const __nv_bfloat16* k_pages;  // [n_pages][Hkv][P][128]
+  const __nv_bfloat16* v_pages;
+  const int* table;              // [B][width]
+  const int* cu;                 // [B + 1]
+  const int* kv;                 // [B]
+  void* out;                     // [T][Hq][128]
+  int4* desc;                    // [C] what a CTA's first tile is, where it ends that tile
+  float* part;                   // [C][2] partial tiles
+  int T, B, Hq, Hkv, G, P, log2P, width, n_pages, max_new, out_dtype;
+  int rows_above, rows_upto;     // the requests of this launch: rows_above < new * G <= rows_upto
+};
+
+constexpr float PG_SCALE_LOG2 = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
+
+BN_DEV float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Request i's new tokens and cache rows; false for lengths that do not fit the call.
+BN_DEV bool paged_request(const PagedArgs& a, int i, int& t0, int& n, int& kv) {
+  t0 = __ldg(a.cu + i);
+  const int t1 = __ldg(a.cu + i + 1);
+  kv = __ldg(a.kv + i);
+  n = t1 - t0;
+  return t0 >= 0 && t1 >= t0 && t1 <= a.T && n <= a.max_new && kv >= 0 && kv <= (long long)a.width * a.P;
+}
+
+// Cache rows that the last row of tile j sees (0 where it sees none).
+template <int M>
+BN_DEV int tile_visible(int n, int kv, int G, int j) {
+  const int last = min((j + 1) * M, n * G) - 1;
+  return max(0, kv - n + last / G + 1);
+}
+template <int M, int U>
+BN_DEV int tile_units(int n, int kv, int G, int j) {
+  return max(1, (tile_visible<M>(n, kv, G, j) + U - 1) / U);
+}
+
+// A CTA's place on the line of units.
+template <int M, int U>
+struct PagedWalk {
+  int seq, t0, n, kv;  // request
+  int head, tile, tiles;
+  int unit;            // next unit of the tile
+  long long pos;       // its place on the line
+  int left;            // units of this CTA still to do
+  int per;             // units per CTA
+
+  // Units of one request and head, or 0 if this launch does not take the request.
+  BN_DEV static int request_units(const PagedArgs& a, int i, bool& bad) {
+    int t0, n, kv;
+    if (!paged_request(a, i, t0, n, kv)) {
+      bad = true;
+      return 0;
+    }
+    const int R = n * a.G;
+    if (R <= a.rows_above || R > a.rows_upto) return 0;
+    int w = 0;
+    for (int j = 0; j * M < R; ++j) w += tile_units<M, U>(n, kv, a.G, j);
+    return w;
+  }
+
+  // Block-wide: finds the CTA's share.  `sm`: 4 long longs, `red`: 32 long longs of shared memory.
+  BN_DEV void begin(const PagedArgs& a, int C, long long* sm, long long* red) {
+    bool bad = false;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    long long mine = 0;
+    for (int i = threadIdx.x; i < a.B; i += blockDim.x) mine += request_units(a, i, bad);
+    const long long total = block_reduce(mine, red, AddOpLL()) * a.Hkv;
+    if (bad && blockIdx.x == 0) flag_index_error();
+    if (threadIdx.x == 0) sm[0] = -1;
+    __syncthreads();
+    const long long share = (total + C - 1) / C;
+    per = (int)share;
+    pos = (long long)blockIdx.x * share;
+    left = (int)max(0ll, min(share, total - pos));
+    if (left == 0) return;
+    long long before = 0;
+    for (int i0 = 0; i0 < a.B; i0 += blockDim.x) {
+      const int i = i0 + threadIdx.x;
+      const long long w = i < a.B ? (long long)request_units(a, i, bad) * a.Hkv : 0;
+      long long v = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+      }
+      if (lane == 31) red[warp] = v;
+      __syncthreads();
+      long long base = before, all = before;
+      for (int k = 0; k < nw; ++k) {
+        if (k < warp) base += red[k];
+        all += red[k];
+      }
+      const long long end = base + v;
+      if (pos >= end - w && pos < end) {
+        sm[0] = i;
+        sm[1] = pos - (end - w);
+        sm[2] = w / a.Hkv;
+      }
+      __syncthreads();
+      before = all;
+      if (sm[0] >= 0) break;
+    }
+    seq = (int)sm[0];
+    const long long off = sm[1];
+    const int w = (int)sm[2];
+    paged_request(a, seq, t0, n, kv);
+    tiles = (n * a.G + M - 1) / M;
+    head = (int)(off / w);
+    int rem = (int)(off - (long long)head * w);
+    tile = 0;
+    for (;;) {
+      const int u = tile_units<M, U>(n, kv, a.G, tile);
+      if (rem < u) break;
+      rem -= u;
+      ++tile;
+    }
+    unit = rem;
+  }
+
+  BN_DEV int units(const PagedArgs& a) const { return tile_units<M, U>(n, kv, a.G, tile); }
+
+  // Goes on behind `cnt` units of the tile.
+  BN_DEV void advance(const PagedArgs& a, int cnt, int tile_total) {
+    left -= cnt;
+    pos += cnt;
+    unit += cnt;
+    if (left == 0 || unit < tile_total) return;
+    unit = 0;
+    if (++tile < tiles) return;
+    tile = 0;
+    if (++head < a.Hkv) return;
+    head = 0;
+    for (;;) {  // units are left, so a request of this launch follows
+      ++seq;
+      if (!paged_request(a, seq, t0, n, kv)) continue;
+      const int R = n * a.G;
+      if (R > a.rows_above && R <= a.rows_upto) break;
+    }
+    tiles = (n * a.G + M - 1) / M;
+  }
+};
+
+// ------------------------------------------------------------------ few rows: mma.sync
+// Requests with few query rows (single tokens, short drafts) are bound by the read of their cache
+// rows.  A CTA of four warps takes tiles of 16 query rows and units of 64 cache rows; each warp
+// works through its own 16 cache rows of every unit with its own running maximum, sum and
+// weighted values, so the warps never wait for one another inside a tile; they are joined at
+// the tile's end.  Each warp copies its rows (4 KB of keys, 4 KB of values, inside one page
+// because page sizes are multiples of 16) through a ring of PD_STAGES stages of its own with
+// cp.async, two stages ahead; two CTAs fit an SM, so 128 KB are in flight per SM.  Rows of 256
+// bytes are stored with their 16-byte chunks permuted by the row (chunk ^ row % 8), which keeps
+// the ldmatrix reads free of bank conflicts; rows behind the visible ones are filled with
+// zeros, so what the cache holds there (NaN included) is never used.
+// Products are m16n8k16 bf16 with fp32 sums; the probabilities enter the second product as the
+// sum of two bf16 (p rounded, and what that left over), so their rounding is 2^-17 of p; the
+// extra instruction is free beside the read.
+constexpr int PD_M = 16;
+constexpr int PD_U = 64;
+constexpr int PD_WARPS = 4;
+constexpr int PD_THREADS = 32 * PD_WARPS;
+constexpr int PD_STAGES = 3;
+constexpr int PD_STAGE_BYTES = 2 * 16 * 256;
+constexpr int PD_RING = PD_WARPS * PD_STAGES * PD_STAGE_BYTES;
+static_assert((64 + 4) * 32 * 4 <= PD_STAGES * PD_STAGE_BYTES, "a warp's fragments fit its drained ring at the join");
+constexpr int PD_PART = PD_M * (PG_D + 2);      // floats of a partial tile: values, maxima, sums
+
+BN_DEV void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+BN_DEV void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+BN_DEV void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16 bytes global -> shared, or 16 zero bytes where !valid (src is not read then).
+BN_DEV void cp_async16_or_zero(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+template <int N>
+BN_DEV void cp_async_wait_group() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+BN_DEV uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 w = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&w);
+}
+
+__global__ void __launch_bounds__(PD_THREADS, 2) k_attn_paged_few(const PagedArgs a) {
+  extern __shared__ __align__(128) uint8_t pd_sm[];
+  __shared__ long long s_walk[4], s_red[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+  pdl_wait();
+  PagedWalk<PD_M, PD_U> w;
+  w.begin(a, gridDim.x, s_walk, s_red);
+  if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  const uint32_t ring = smem_addr(pd_sm) + warp * PD_STAGES * PD_STAGE_BYTES;
+  const int g = lane >> 2, tq = lane & 3;
+  const long long page_elems = (long long)a.Hkv * a.P * PG_D;
+
+  while (w.left > 0) {
+    const int nu = w.units(a);
+    const int cnt = min(w.left, nu - w.unit);
+    const int R = w.n * a.G, r0 = w.tile * PD_M;
+    const int vis = tile_visible<PD_M>(w.n, w.kv, a.G, w.tile);
+    // this thread's two query rows (g and g + 8 of the tile): what they see, and their q fragments
+    int lim[2];
+    uint32_t qf[8][4];
+    long long qoff[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = r0 + g + 8 * e;
+      const bool there = r < R;
+      const int t = there ? r / a.G : 0, hg = there ? r - t * a.G : 0;
+      lim[e] = there ? max(0, w.kv - w.n + t + 1) : 0;
+      qoff[e] = there ? ((long long)(w.t0 + t) * a.Hq + w.head * a.G + hg) * PG_D : -1;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + qoff[e] + ks * 16 + 2 * tq);
+        qf[ks][e] = there ? __ldg(src) : 0u;
+        qf[ks][e + 2] = there ? __ldg(src + 4) : 0u;
+      }
+    }
+    float O[16][4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) O[i][0] = O[i][1] = O[i][2] = O[i][3] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+    // page ids, 32 units at a time: lane i holds the page of unit ids0 + i (this warp's rows)
+    const int* trow = a.table + (long long)w.seq * a.width;
+    int ids = -1, ids0 = w.unit - 32;
+    auto load = [&](int u, int stage) {
+      if (u >= ids0 + 32) {
+        ids0 = u;
+        const long long row = (long long)(u + lane) * PD_U + warp * 16;
+        ids = -1;
+        if (row < vis) {
+          ids = __ldg(trow + (row >> a.log2P));
+          if (ids < 0 || ids >= a.n_pages) {
+            ids = -1;
+            flag_index_error();
+          }
+        }
+      }
+      const int page = __shfl_sync(0xffffffffu, ids, u - ids0);
+      const int row0 = u * PD_U + warp * 16;
+      const long long base = (long long)max(page, 0) * page_elems + ((long long)w.head * a.P + (row0 & (a.P - 1))) * PG_D;
+      const uint32_t dst = ring + stage * PD_STAGE_BYTES;
+      const int ch = lane & 15;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = 2 * i + (lane >> 4);
+        const bool ok = page >= 0 && row0 + row < vis;
+        const long long off = base + row * PG_D + ch * 8;
+        const uint32_t d = dst + row * 256 + ((ch ^ (row & 7)) << 4);
+        cp_async16_or_zero(d, a.k_pages + (ok ? off : 0), ok);
+        cp_async16_or_zero(d + 4096, a.v_pages + (ok ? off : 0), ok);
+      }
+    };
+#pragma unroll
+    for (int s = 0; s < PD_STAGES - 1; ++s) {
+      if (s < cnt) load(w.unit + s, s);
+      cp_async_commit();
+    }
+    int st = 0;
+    for (int it = 0; it < cnt; ++it) {
+      cp_async_wait_group<PD_STAGES - 2>();
+      __syncwarp();
+      if (it + PD_STAGES - 1 < cnt) load(w.unit + it + PD_STAGES - 1, st == 0 ? PD_STAGES - 1 : st - 1);
+      cp_async_commit();
+      const uint32_t kb = ring + st * PD_STAGE_BYTES, vb = kb + 4096;
+      float S[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+      {
+        const int row = (lane & 7) + ((lane >> 4) << 3), c1 = (lane >> 3) & 1;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          uint32_t b[4];
+          ldmatrix_x4(b, kb + row * 256 + (((2 * ks + c1) ^ (row & 7)) << 4));
+          mma_bf16(S[0], qf[ks], b[0], b[1]);
+          mma_bf16(S[1], qf[ks], b[2], b[3]);
+        }
+      }
+      const int col0 = (w.unit + it) * PD_U + warp * 16 + 2 * tq;
+      uint32_t ph[4], pl[4];
+      float alpha[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int col = col0 + (i >> 1) * 8 + (i & 1);
+          x[i] = col < lim[e] ? __fmul_rn(S[i >> 1][2 * e + (i & 1)], PG_SCALE_LOG2) : -INFINITY;
+        }
+        float mt = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+        const float mn = fmaxf(m[e], mt);
+        const float mu = mn == -INFINITY ? 0.0f : mn;  // a row that has seen nothing yet: all weights 0
+        alpha[e] = exp2_approx(__fsub_rn(m[e], mu));
+        m[e] = mn;
+        float p[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[i] = exp2_approx(__fsub_rn(x[i], mu));
+          hi[i] = __bfloat162float(__float2bfloat16_rn(p[i]));
+        }
+        l[e] = __fmaf_rn(l[e], alpha[e], __fadd_rn(__fadd_rn(p[0], p[1]), __fadd_rn(p[2], p[3])));
+        ph[e] = pack_bf16(hi[0], hi[1]);
+        ph[e + 2] = pack_bf16(hi[2], hi[3]);
+        pl[e] = pack_bf16(__fsub_rn(p[0], hi[0]), __fsub_rn(p[1], hi[1]));
+        pl[e + 2] = pack_bf16(__fsub_rn(p[2], hi[2]), __fsub_rn(p[3], hi[3]));
+      }
+      if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          O[i][0] = __fmul_rn(O[i][0], alpha[0]);
+          O[i][1] = __fmul_rn(O[i][1], alpha[0]);
+          O[i][2] = __fmul_rn(O[i][2], alpha[1]);
+          O[i][3] = __fmul_rn(O[i][3], alpha[1]);
+        }
+      }
+      {
+        const int row = (lane & 7) + (((lane >> 3) & 1) << 3), c1 = lane >> 4;
+#pragma unroll
+        for (int dt = 0; dt < 8; ++dt) {
+          uint32_t b[4];
+          ldmatrix_x4_trans(b, vb + row * 256 + (((2 * dt + c1) ^ (row & 7)) << 4));
+          mma_bf16(O[2 * dt], ph, b[0], b[1]);
+          mma_bf16(O[2 * dt + 1], ph, b[2], b[3]);
+          mma_bf16(O[2 * dt], pl, b[0], b[1]);
+          mma_bf16(O[2 * dt + 1], pl, b[2], b[3]);
+        }
+      }
+      if (++st == PD_STAGES) st = 0;
+    }
+    cp_async_wait_all();
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] = __fadd_rn(l[e], __shfl_xor_sync(0xffffffffu, l[e], 1));
+      l[e] = __fadd_rn(l[e], __shfl_xor_sync(0xffffffffu, l[e], 2));
+    }
+    // join the four warps: 1 into 0 and 3 into 2, then 2 into 0, through the giver's ring (drained)
+#pragma unroll
+    for (int step = 1; step <= 2; ++step) {
+      const bool gives = (warp & (2 * step - 1)) == step, takes = (warp & (2 * step - 1)) == 0;
+      float* buf = reinterpret_cast<float*>(pd_sm + (warp | step) * PD_STAGES * PD_STAGE_BYTES) + lane;
+      if (gives) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) buf[i * 32] = O[i >> 2][i & 3];
+        buf[64 * 32] = m[0];
+        buf[65 * 32] = m[1];
+        buf[66 * 32] = l[0];
+        buf[67 * 32] = l[1];
+      }
+      __syncthreads();
+      if (takes) {
+        float f[2], h[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float mo = buf[(64 + e) * 32], mn = fmaxf(m[e], mo);
+          const float mu = mn == -INFINITY ? 0.0f : mn;
+          f[e] = exp2_approx(__fsub_rn(m[e], mu));
+          h[e] = exp2_approx(__fsub_rn(mo, mu));
+          m[e] = mn;
+          l[e] = __fmaf_rn(l[e], f[e], __fmul_rn(buf[(66 + e) * 32], h[e]));
+        }
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          const int e = (i >> 1) & 1;
+          O[i >> 2][i & 3] = __fmaf_rn(O[i >> 2][i & 3], f[e], __fmul_rn(buf[i * 32], h[e]));
+        }
+      }
+      __syncthreads();  // the ring is filled again for the next tile
+    }
+    if (warp == 0) {
+      if (cnt == nu) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (qoff[e] < 0) continue;
+          const float inv = l[e] > 0.0f ? __fdiv_rn(1.0f, l[e]) : (l[e] == 0.0f ? 0.0f : l[e]);  // NaN stays
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float x = __fmul_rn(O[i][2 * e], inv), y = __fmul_rn(O[i][2 * e + 1], inv);
+            const long long off = qoff[e] + i * 8 + 2 * tq;
+            if (a.out_dtype == BITNET_BF16)
+              *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) + off) = pack_bf16(x, y);
+            else
+              *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + off) = make_float2(x, y);
+          }
+        }
+      } else {
+        float* part = a.part + ((long long)blockIdx.x * 2 + (w.unit > 0 ? 0 : 1)) * PD_PART;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            *reinterpret_cast<float2*>(part + (g + 8 * e) * PG_D + i * 8 + 2 * tq) = make_float2(O[i][2 * e], O[i][2 * e + 1]);
+          if (tq == 0) {
+            part[PD_M * PG_D + g + 8 * e] = m[e];
+            part[PD_M * PG_D + PD_M + g + 8 * e] = l[e];
+          }
+        }
+        if (lane == 0 && w.unit > 0 && w.unit + cnt == nu)
+          a.desc[blockIdx.x] = make_int4((int)((w.pos - w.unit) / w.per), w.seq, w.head, w.tile);
+      }
+    }
+    w.advance(a, cnt, nu);
+  }
+}
+
+// Joins the parts of the tile that CTA c finished: part 1 of the CTA that the tile began in, and
+// part 0 of every later one up to c.  Thread: a row and eight of its dimensions.
+__global__ void __launch_bounds__(256) k_attn_paged_few_join(const PagedArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int c = blockIdx.x;
+  const int4 d = a.desc[c];
+  if (d.x < 0) return;
+  int t0, n, kv;
+  paged_request(a, d.y, t0, n, kv);
+  const int row = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * 8;
+  const int r = d.w * PD_M + row;
+  if (r >= n * a.G) return;
+  auto part = [&](int i) { return a.part + ((long long)i * 2 + (i == d.x ? 1 : 0)) * PD_PART; };
+  float m = -INFINITY;
+  for (int i = d.x; i <= c; ++i) m = fmaxf(m, part(i)[PD_M * PG_D + row]);
+  const float mu = m == -INFINITY ? 0.0f : m;
+  float l = 0.0f, o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = d.x; i <= c; ++i) {
+    const float* p = part(i);
+    const float f = exp2_approx(__fsub_rn(p[PD_M * PG_D + row], mu));
+    l = __fmaf_rn(p[PD_M * PG_D + PD_M + row], f, l);
+    const float4 x = *reinterpret_cast<const float4*>(p + row * PG_D + d0);
+    const float4 y = *reinterpret_cast<const float4*>(p + row * PG_D + d0 + 4);
+    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] = __fmaf_rn(v[k], f, o[k]);
+  }
+  const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);
+  const int t = r / a.G;
+  const long long off = ((long long)(t0 + t) * a.Hq + d.z * a.G + (r - t * a.G)) * PG_D + d0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) o[k] = __fmul_rn(o[k], inv);
+  if (a.out_dtype == BITNET_BF16) {
+    *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + off) =
+        make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+  } else {
+    float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + off);
+    dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+}  // namespace bitnet

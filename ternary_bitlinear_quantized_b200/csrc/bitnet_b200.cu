@@ -3,6 +3,7 @@
 // kernels of quant.cuh, pack.cuh, engine.cuh and gemm_tc.cuh (one translation unit, so
 // that the device status word needs no relocatable device code).
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -17,6 +18,8 @@
 #include "gemm_tc.cuh"
 #include "shard.cuh"
 #include "attention.cuh"
+#include "paged.cuh"
+#include "attn_paged.cuh"
 
 namespace bitnet {
 
@@ -133,12 +136,12 @@ static bitnet_status enqueue_quant(const void* x, bitnet_dtype xt, const float* 
       auto* kern = w == 1 ? k_rmsnorm_quant_warps<__nv_bfloat16, 1>
                           : (w == 2 ? k_rmsnorm_quant_warps<__nv_bfloat16, 2> : k_rmsnorm_quant_warps<__nv_bfloat16, 4>);
       e = launch(kern, dim3(grid), dim3(QW_THREADS), 0, s, true, reinterpret_cast<const __nv_bfloat16*>(x), gain, eps,
-                 (int)T, (int)K, q, s_x, sum_q);
+                 (int)T, (int)K, q, s_x, sum_q, (const void*)nullptr, (void*)nullptr);
     } else {
       auto* kern = w == 1 ? k_rmsnorm_quant_warps<float, 1>
                           : (w == 2 ? k_rmsnorm_quant_warps<float, 2> : k_rmsnorm_quant_warps<float, 4>);
       e = launch(kern, dim3(grid), dim3(QW_THREADS), 0, s, true, reinterpret_cast<const float*>(x), gain, eps, (int)T,
-                 (int)K, q, s_x, sum_q);
+                 (int)K, q, s_x, sum_q, (const void*)nullptr, (void*)nullptr);
     }
     if (e != cudaSuccess) return cuda_fail(e, "k_rmsnorm_quant_warps");
     return BITNET_OK;
@@ -185,13 +188,53 @@ static bitnet_status enqueue_quant(const void* x, bitnet_dtype xt, const float* 
   }
   if (xt == BITNET_BF16) {
     e = launch(k_rmsnorm_quant<__nv_bfloat16>, dim3((unsigned)T), dim3(threads), smem, s, true,
-               reinterpret_cast<const __nv_bfloat16*>(x), gain, eps, (int)K, q, s_x, sum_q, vec);
+               reinterpret_cast<const __nv_bfloat16*>(x), gain, eps, (int)K, q, s_x, sum_q, vec,
+               (const void*)nullptr, (void*)nullptr);
   } else {
     e = launch(k_rmsnorm_quant<float>, dim3((unsigned)T), dim3(threads), smem, s, true,
-               reinterpret_cast<const float*>(x), gain, eps, (int)K, q, s_x, sum_q, vec);
+               reinterpret_cast<const float*>(x), gain, eps, (int)K, q, s_x, sum_q, vec,
+               (const void*)nullptr, (void*)nullptr);
   }
   if (e != cudaSuccess) return cuda_fail(e, "k_rmsnorm_quant");
   return BITNET_OK;
+}
+
+// Residual addition in front of the norm: the same choice of kernel as enqueue_quant, without the
+// double-buffered one for long fp32 rows (a residual stream is a model's hidden width).
+template <typename TIn, typename TRes>
+static bitnet_status enqueue_add_quant(const void* x, const void* r_in, void* r_out, const float* gain, float eps,
+                                       int64_t T, int64_t K, int8_t* q, float* s_x, int32_t* sum_q, cudaStream_t s) {
+  const TIn* xp = reinterpret_cast<const TIn*>(x);
+  const TRes* rp = reinterpret_cast<const TRes*>(r_in);
+  TRes* op = reinterpret_cast<TRes*>(r_out);
+  cudaError_t e;
+  if (K <= 4 * 2048 && K % 8 == 0) {  // every row 16-byte aligned in all three types
+    const int w = (T <= 256 || K > 4096) ? 4 : (K <= 2048 ? 1 : 2);
+    const int rows = QW_THREADS / 32 / w;
+    auto* kern = w == 1 ? k_rmsnorm_quant_warps<TIn, 1, TRes>
+                        : (w == 2 ? k_rmsnorm_quant_warps<TIn, 2, TRes> : k_rmsnorm_quant_warps<TIn, 4, TRes>);
+    e = launch(kern, dim3((unsigned)((T + rows - 1) / rows)), dim3(QW_THREADS), 0, s, true, xp, gain, eps, (int)T,
+               (int)K, q, s_x, sum_q, rp, op);
+    return e == cudaSuccess ? BITNET_OK : cuda_fail(e, "k_rmsnorm_quant_warps (residual)");
+  }
+  int threads = (int)((K / 8 + 31) / 32 * 32);
+  threads = threads < 128 ? 128 : (threads > 1024 ? 1024 : threads);
+  const size_t smem = (size_t)K * sizeof(float);
+  auto* kern = k_rmsnorm_quant<TIn, TRes>;
+  if (smem > 48 * 1024) {
+    static std::atomic<int> done_dev[64] = {};  // one set per instance of this template
+    int dev = 0;
+    cudaGetDevice(&dev);
+    std::atomic<int>& done = done_dev[dev & 63];
+    if (!done.load(std::memory_order_acquire)) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BITNET_MAX_K * 4);
+      if (e != cudaSuccess) return cuda_fail(e, "quant attribute (residual)");
+      done.store(1, std::memory_order_release);
+    }
+  }
+  e = launch(kern, dim3((unsigned)T), dim3(threads), smem, s, true, xp, gain, eps, (int)K, q, s_x, sum_q,
+             (int)(K % 8 == 0), rp, op);
+  return e == cudaSuccess ? BITNET_OK : cuda_fail(e, "k_rmsnorm_quant (residual)");
 }
 
 // ------------------------------------------------------------------ product
@@ -1190,6 +1233,146 @@ bitnet_status bitnet_decoder_block(const void* x, const void* attn_out, bitnet_d
   return enqueue_engine(ea, s);
 }
 
+// ---------------------------------------------------------------- paged serving step
+bitnet_status bitnet_add_rmsnorm_quant_act(const void* x, bitnet_dtype xt, const void* residual, bitnet_dtype rt,
+                                           const float* gain, float eps, int64_t T, int64_t K, void* residual_out,
+                                           int8_t* q, float* s_x, int32_t* sum_q, bitnet_stream stream) {
+  if ((xt != BITNET_BF16 && xt != BITNET_F32) || (rt != BITNET_BF16 && rt != BITNET_F32)) return BITNET_ERR_DTYPE;
+  if (T < 0 || K <= 0 || K > BITNET_MAX_K || T > 0x7FFFFFFFll) return BITNET_ERR_SHAPE;
+  if (T == 0) return BITNET_OK;
+  if (!x || !residual || !residual_out || !q || !s_x || !sum_q) return BITNET_ERR_NULL;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(residual_out) || !aligned16(q) || !aligned16(s_x) ||
+      !aligned16(sum_q) || (gain && !aligned16(gain)))
+    return BITNET_ERR_ALIGN;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  auto* run = xt == BITNET_BF16
+                  ? (rt == BITNET_BF16 ? enqueue_add_quant<__nv_bfloat16, __nv_bfloat16> : enqueue_add_quant<__nv_bfloat16, float>)
+                  : (rt == BITNET_BF16 ? enqueue_add_quant<float, __nv_bfloat16> : enqueue_add_quant<float, float>);
+  return run(x, residual, residual_out, gain, eps, T, K, q, s_x, sum_q, s);
+}
+
+static int page_log2(int64_t P) {  // 4..8 for 16..256, else -1
+  for (int l = 4; l <= 8; ++l)
+    if (P == (1ll << l)) return l;
+  return -1;
+}
+
+bitnet_status bitnet_paged_plan(const int32_t* new_lens, const int32_t* ctx_lens, int64_t B, int64_t page_size,
+                                int32_t* block_table, int64_t width, const int32_t* free_pages, int64_t n_list,
+                                const int32_t* n_free, int64_t T, int32_t* cu_new, int32_t* kv_lens,
+                                int32_t* positions, int32_t* slots, int32_t* n_free_out, bitnet_stream stream) {
+  if (B < 0 || B > BITNET_MAX_REQUESTS || T < 0 || T > BITNET_MAX_STEP_TOKENS || page_log2(page_size) < 0 ||
+      width <= 0 || width * page_size > 0x7FFFFFFFll || n_list < 0 || n_list > 0x7FFFFFFFll)
+    return BITNET_ERR_SHAPE;
+  if (!cu_new || !n_free || !n_free_out || (B > 0 && (!new_lens || !ctx_lens || !block_table || !kv_lens)) ||
+      (n_list > 0 && !free_pages) || (T > 0 && (!positions || !slots)))
+    return BITNET_ERR_NULL;
+  for (const void* p : {(const void*)new_lens, (const void*)ctx_lens, (const void*)block_table, (const void*)free_pages,
+                        (const void*)n_free, (const void*)cu_new, (const void*)kv_lens, (const void*)positions,
+                        (const void*)slots, (const void*)n_free_out})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return BITNET_ERR_ALIGN;
+  const long long ctas = (T + PLAN_TOKENS - 1) / PLAN_TOKENS;
+  const cudaError_t e = launch(k_paged_plan, dim3((unsigned)(ctas > 0 ? ctas : 1)), dim3(PLAN_THREADS),
+                               (size_t)(B + 1) * 8, reinterpret_cast<cudaStream_t>(stream), true, new_lens, ctx_lens,
+                               (int)B, (int)page_size, block_table, (int)width, free_pages, (int)n_list, n_free, (int)T,
+                               cu_new, kv_lens, positions, slots, n_free_out);
+  return e == cudaSuccess ? BITNET_OK : cuda_fail(e, "k_paged_plan");
+}
+
+bitnet_status bitnet_rope_paged_append(const void* q, const void* k, const void* v, bitnet_dtype xt, int64_t T,
+                                       int64_t Hq, int64_t Hkv, int64_t d, const int32_t* positions,
+                                       const int32_t* slots, double theta, void* q_rot, void* k_pages, void* v_pages,
+                                       int64_t n_pages, int64_t page_size, bitnet_stream stream) {
+  if (xt != BITNET_BF16 && xt != BITNET_F32) return BITNET_ERR_DTYPE;
+  if (T < 0 || T > BITNET_MAX_STEP_TOKENS || Hq <= 0 || Hkv <= 0 || Hq > 1024 || Hq % Hkv || d != PG_D ||
+      page_log2(page_size) < 0 || n_pages <= 0 || n_pages * page_size > 0x7FFFFFFFll || !(theta > 0.0))
+    return BITNET_ERR_SHAPE;
+  if (T == 0) return BITNET_OK;
+  if (!q || !k || !v || !positions || !slots || !q_rot || !k_pages || !v_pages) return BITNET_ERR_NULL;
+  for (const void* p : {q, k, v, (const void*)q_rot, (const void*)k_pages, (const void*)v_pages})
+    if (!aligned16(p)) return BITNET_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(positions) & 3u) || (reinterpret_cast<uintptr_t>(slots) & 3u)) return BITNET_ERR_ALIGN;
+  RopeTurns turns;
+  for (int i = 0; i < PG_D / 2; ++i) turns.g[i] = std::pow(theta, -2.0 * i / PG_D) / 6.283185307179586476925;
+  const dim3 grid((unsigned)((T + ROPE_TOKENS - 1) / ROPE_TOKENS)), block(ROPE_THREADS);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  __nv_bfloat16 *qo = reinterpret_cast<__nv_bfloat16*>(q_rot), *ko = reinterpret_cast<__nv_bfloat16*>(k_pages),
+                *vo = reinterpret_cast<__nv_bfloat16*>(v_pages);
+  cudaError_t e;
+  if (xt == BITNET_BF16) {
+    typedef const __nv_bfloat16* P;
+    e = launch(k_rope_paged<__nv_bfloat16>, grid, block, 0, s, true, (P)q, (P)k, (P)v, positions, slots, (int)T, (int)Hq,
+               (int)Hkv, (int)page_size, (long long)(n_pages * page_size), turns, qo, ko, vo);
+  } else {
+    typedef const float* P;
+    e = launch(k_rope_paged<float>, grid, block, 0, s, true, (P)q, (P)k, (P)v, positions, slots, (int)T, (int)Hq,
+               (int)Hkv, (int)page_size, (long long)(n_pages * page_size), turns, qo, ko, vo);
+  }
+  return e == cudaSuccess ? BITNET_OK : cuda_fail(e, "k_rope_paged");
+}
+
+// The workspace: the few-row launch's tile descriptors (16 bytes per CTA) and partial tiles.
+static int paged_few_ctas() { return 2 * device_sm_count(); }
+
+size_t bitnet_attention_paged_workspace_bytes(int64_t Hq, int64_t Hkv, int64_t max_new) {
+  if (Hq <= 0 || Hkv <= 0 || Hq > 1024 || Hq % Hkv || max_new < 0) return 0;
+  const size_t few = (size_t)paged_few_ctas();
+  return align_up(few * 16) + align_up(few * 2 * PD_PART * 4);
+}
+
+bitnet_status bitnet_attention_paged(const void* q_rot, const void* k_pages, const void* v_pages,
+                                     const int32_t* block_table, const int32_t* cu_new, const int32_t* kv_lens,
+                                     int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t d, int64_t n_pages,
+                                     int64_t page_size, int64_t width, int64_t max_new, void* out, bitnet_dtype ot,
+                                     void* ws, size_t ws_bytes, bitnet_stream stream) {
+  if (ot != BITNET_BF16 && ot != BITNET_F32) return BITNET_ERR_DTYPE;
+  const int log2P = page_log2(page_size);
+  if (T < 0 || T > BITNET_MAX_STEP_TOKENS || B < 0 || B > BITNET_MAX_REQUESTS || Hq <= 0 || Hkv <= 0 || Hq > 1024 ||
+      Hq % Hkv || d != PG_D || log2P < 0 || n_pages <= 0 || n_pages * page_size > 0x7FFFFFFFll || width <= 0 ||
+      width * page_size > 0x7FFFFFFFll || max_new < 0)
+    return BITNET_ERR_SHAPE;
+  if (T == 0 || B == 0 || max_new == 0) return BITNET_OK;
+  if (!q_rot || !k_pages || !v_pages || !block_table || !cu_new || !kv_lens || !out) return BITNET_ERR_NULL;
+  if (!ws || ws_bytes < bitnet_attention_paged_workspace_bytes(Hq, Hkv, max_new)) return BITNET_ERR_WORKSPACE;
+  for (const void* p : {q_rot, k_pages, v_pages, (const void*)out, (const void*)ws})
+    if (!aligned16(p)) return BITNET_ERR_ALIGN;
+  for (const void* p : {(const void*)block_table, (const void*)cu_new, (const void*)kv_lens})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return BITNET_ERR_ALIGN;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  PagedArgs a = {};
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q_rot);
+  a.k_pages = reinterpret_cast<const __nv_bfloat16*>(k_pages);
+  a.v_pages = reinterpret_cast<const __nv_bfloat16*>(v_pages);
+  a.table = block_table;
+  a.cu = cu_new;
+  a.kv = kv_lens;
+  a.out = out;
+  a.T = (int)T;
+  a.B = (int)B;
+  a.Hq = (int)Hq;
+  a.Hkv = (int)Hkv;
+  a.G = (int)(Hq / Hkv);
+  a.P = (int)page_size;
+  a.log2P = log2P;
+  a.width = (int)width;
+  a.n_pages = (int)n_pages;
+  a.max_new = (int)(max_new < T ? max_new : T);
+  a.out_dtype = ot;
+  uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+  const int few = paged_few_ctas();
+  a.desc = reinterpret_cast<int4*>(w);
+  a.part = reinterpret_cast<float*>(w + align_up((size_t)few * 16));
+  a.rows_above = 0;
+  a.rows_upto = 0x7FFFFFFF;
+  cudaError_t e = opt_in_smem((const void*)k_attn_paged_few, 8);
+  if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_few attribute");
+  e = launch(k_attn_paged_few, dim3((unsigned)few), dim3(PD_THREADS), PD_RING, s, true, a);
+  if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_few");
+  e = launch(k_attn_paged_few_join, dim3((unsigned)few), dim3(256), 0, s, true, a);
+  if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_few_join");
+  return BITNET_OK;
+}
+
 bitnet_status bitnet_debug_set_wait_limit(long long cycles) {
   if (cycles <= 0) cycles = kDefaultWaitLimitCycles;
   BN_CUDA(cudaDeviceSynchronize(), "wait limit (synchronize)");
@@ -1218,6 +1401,7 @@ const char* bitnet_status_string(bitnet_status st) {
     case BITNET_ERR_WORKSPACE: return "workspace missing or too small";
     case BITNET_ERR_CUDA: return "CUDA error";
     case BITNET_ERR_TIMEOUT: return "kernel wait timed out";
+    case BITNET_ERR_INDEX: return "device-side length, page or slot out of range";
   }
   return "unknown status";
 }

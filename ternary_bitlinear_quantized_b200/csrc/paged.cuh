@@ -1,0 +1,266 @@
+// The paged key/value cache of a serving step over many requests: which pages and rows the
+// step's tokens go to (k_paged_plan), and the rotary embedding with the append to those rows
+// (k_rope_paged).  The cache is k_pages / v_pages, bf16 [pages][Hkv][page_size][128]; slot s
+// names row s % page_size of page s / page_size, in every key/value head.  The attention that
+// reads the cache is in attn_paged.cuh.
+//
+// Lengths, tables, slots and page ids live on the device, so no step waits for the host; what
+// the host cannot check the kernels do: an index out of range is skipped and the device status
+// word set to BITNET_ERR_INDEX.
+#pragma once
+#include "common.cuh"
+#include "quant.cuh"
+
+namespace bitnet {
+
+constexpr int PG_D = 128;               // head size
+constexpr int PG_MAX_REQUESTS = 4096;   // k_paged_plan keeps two prefix sums of this many requests in shared memory
+
+BN_DEV void flag_index_error() { atomicExch(&g_device_status, (int)BITNET_ERR_INDEX); }
+
+// Inclusive prefix sum over the block of one int per thread; `total` is the block's sum.
+// `scratch`: 32 ints of shared memory; ends with a barrier that protects it.
+BN_DEV int block_scan_incl(int v, int* scratch, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) scratch[warp] = v;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int w = 0; w < nw; ++w) {
+    const int s = scratch[w];
+    if (w < warp) before += s;
+    all += s;
+  }
+  __syncthreads();
+  total = all;
+  return v + before;
+}
+
+// Largest i in [0, n) with a[i] <= x, for ascending a with a[0] <= x.
+BN_DEV int last_not_above(const int* a, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// ------------------------------------------------------------------ the step's plan
+// need_i = ceil((ctx_i + new_i) / P) - ceil(ctx_i / P) pages are taken from the top of the free
+// list, request by request: with start_i the sum of the needs before i, page j of request i is
+// free[n_free - 1 - start_i - j].  Token t of the step belongs to the request i with
+// cu_i <= t < cu_{i+1}; its position is ctx_i + t - cu_i and its slot table[i][pos / P] P + pos % P.
+//
+// Bound by latency (a few dependent loads and two scans; the largest steps write two ints a
+// token).  So it is one launch: every CTA makes both prefix sums for itself (B lengths are a few
+// KB from L2) and then writes its share of the tokens and of the new table entries; a token's new
+// page is read from the free list directly, not from the table entry that another CTA may be
+// writing.
+constexpr int PLAN_THREADS = 256;
+constexpr int PLAN_TOKENS = 1024;  // tokens per CTA
+__global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const int* __restrict__ new_lens, const int* __restrict__ ctx_lens,
+                                                             int B, int P, int* table, int width,
+                                                             const int* __restrict__ free_pages, int n_list,
+                                                             const int* __restrict__ n_free, int T, int* __restrict__ cu_out,
+                                                             int* __restrict__ kv_out, int* __restrict__ pos_out,
+                                                             int* __restrict__ slot_out, int* __restrict__ n_free_out) {
+  extern __shared__ int plan_sm[];
+  __shared__ int scratch[32];
+  int* cu = plan_sm;            // [B + 1] tokens before request i
+  int* start = plan_sm + B + 1; // [B + 1] new pages before request i
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long cap = (long long)width * P;
+  bool bad = false;
+  int nf = __ldg(n_free);
+  if (nf < 0 || nf > n_list) {
+    bad = true;
+    nf = 0;
+  }
+  // A request's lengths; one that does not fit its row of the table keeps its place among the
+  // tokens, but gets no pages and no slots.
+  auto read = [&](int i, int& n, int& c, bool& fits) {
+    n = __ldg(new_lens + i);
+    c = __ldg(ctx_lens + i);
+    fits = true;
+    if (n < 0 || c < 0 || c + (long long)n > cap) {
+      bad = true;
+      fits = false;
+      n = max(n, 0);
+      c = (int)min((long long)max(c, 0), cap);
+    }
+    if (n > T) {  // keeps the sums in range
+      bad = true;
+      n = T;
+    }
+  };
+  // slot of row r of a page; ids below 0 stand for no page, others must keep the slot an int32
+  auto slot_of = [&](int page, int r) {
+    if (page > (0x7FFFFFFF - r) / P) {
+      bad = true;
+      return -1;
+    }
+    return page < 0 ? -1 : page * P + r;
+  };
+  long long tok = 0, pg = 0;
+  for (int i0 = 0; i0 < B; i0 += PLAN_THREADS) {
+    const int i = i0 + threadIdx.x;
+    int n = 0, need = 0;
+    if (i < B) {
+      int c;
+      bool fits;
+      read(i, n, c, fits);
+      if (fits) need = (c + n + P - 1) / P - (c + P - 1) / P;
+      if (blockIdx.x == 0) kv_out[i] = fits ? c + n : c;
+    }
+    // 32-bit block sums hold: n <= T <= 2^22, need <= n / 16 + 1
+    int tn, tp;
+    const int sn = block_scan_incl(n, scratch, tn), sp = block_scan_incl(need, scratch, tp);
+    if (i < B) {
+      const long long a = tok + sn - n;
+      cu[i] = (int)min(a, (long long)T);
+      start[i] = (int)(pg + sp - need);
+    }
+    tok += tn;
+    pg += tp;
+  }
+  if (tok > T) {
+    bad = true;
+    tok = T;
+  }
+  if (threadIdx.x == 0) {
+    cu[B] = (int)tok;
+    start[B] = (int)pg;
+    if (blockIdx.x == 0) n_free_out[0] = nf - (int)pg;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= B; i += PLAN_THREADS) cu_out[i] = cu[i];
+  // new table entries, over the whole grid
+  const int nthreads = gridDim.x * PLAN_THREADS, gid = blockIdx.x * PLAN_THREADS + threadIdx.x;
+  for (int e = gid; e < (int)pg; e += nthreads) {
+    const int i = last_not_above(start, B, e);
+    const int c = __ldg(ctx_lens + i);
+    const int at = nf - 1 - e;
+    table[(long long)i * width + (c + P - 1) / P + (e - start[i])] = at >= 0 ? __ldg(free_pages + at) : -1;
+  }
+  // tokens
+  const int t1 = min(T, (int)(blockIdx.x + 1) * PLAN_TOKENS);
+  for (int t = blockIdx.x * PLAN_TOKENS + threadIdx.x; t < t1; t += PLAN_THREADS) {
+    int pos = 0, slot = -1;
+    if (t < (int)tok) {
+      const int i = last_not_above(cu, B, t);
+      int n, c;
+      bool fits;
+      read(i, n, c, fits);
+      pos = c + t - cu[i];
+      if (fits) {
+        const int pi = pos / P, old = (c + P - 1) / P;
+        int page;
+        if (pi < old) {
+          page = table[(long long)i * width + pi];
+        } else {
+          const int at = nf - 1 - start[i] - (pi - old);
+          page = at >= 0 ? __ldg(free_pages + at) : -1;
+        }
+        slot = slot_of(page, pos % P);
+      }
+    }
+    pos_out[t] = pos;
+    slot_out[t] = slot;
+  }
+  if (bad) flag_index_error();
+}
+
+// ------------------------------------------------------------------ rotary embedding + append
+// The pair (x_i, x_{i+64}) of q and k turns by a = p theta^(-2i/128).  The host passes
+// g_i = theta^(-2i/128) / (2 pi) in fp64, so a is p g_i turns: its whole turns are dropped in
+// fp64 (p g_i - rint(p g_i) is exact) and sine and cosine of pi times the rest, |rest| <= 1,
+// taken in fp32.  |p g_i| < 2^31, so the fp64 product is off by at most 2^-22 turns there and by
+// 2^-37 at positions below 2^16.  The rotation is fp32, one rounding an operation; q_rot and the
+// cache are bf16 (nearest even).
+//
+// Bound by HBM: each value is read and written once.  A CTA takes ROPE_TOKENS tokens: their 64
+// angles each are made once and shared by all heads (a sine and cosine per head would cost more
+// than the copy), then every thread moves 8 + 8 values of a head with 16-byte accesses.
+constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_TOKENS = 4;
+struct RopeTurns {
+  double g[PG_D / 2];
+};
+template <typename TIn>
+__global__ void __launch_bounds__(ROPE_THREADS) k_rope_paged(const TIn* __restrict__ q, const TIn* __restrict__ k,
+                                                             const TIn* __restrict__ v, const int* __restrict__ positions,
+                                                             const int* __restrict__ slots, int T, int Hq, int Hkv, int P,
+                                                             long long n_slots, const __grid_constant__ RopeTurns turns,
+                                                             __nv_bfloat16* __restrict__ q_rot,
+                                                             __nv_bfloat16* __restrict__ k_pages,
+                                                             __nv_bfloat16* __restrict__ v_pages) {
+  constexpr int HALF = PG_D / 2;
+  __shared__ float s_cos[ROPE_TOKENS][HALF], s_sin[ROPE_TOKENS][HALF];
+  __shared__ int s_slot[ROPE_TOKENS];
+  static_assert(ROPE_TOKENS * HALF == ROPE_THREADS, "one angle a thread");
+  pdl_launch_dependents();
+  pdl_wait();
+  const int t0 = blockIdx.x * ROPE_TOKENS;
+  {
+    const int tt = threadIdx.x / HALF, i = threadIdx.x % HALF, t = t0 + tt;
+    const int slot = t < T ? __ldg(slots + t) : -1;
+    if (i == 0) {
+      s_slot[tt] = slot < n_slots ? slot : -1;
+      if (slot >= n_slots) flag_index_error();
+    }
+    if (slot >= 0) {
+      const double a = __dmul_rn((double)__ldg(positions + t), turns.g[i]);
+      const float r = __double2float_rn(__dsub_rn(a, rint(a)));
+      sincospif(__fmul_rn(2.0f, r), &s_sin[tt][i], &s_cos[tt][i]);
+    }
+  }
+  __syncthreads();
+  const int H = Hq + 2 * Hkv;
+  const int units = H * 8;  // (head, 8-value chunk of its lower half with the chunk 64 above)
+  auto pack = [](float a, float b) {
+    const __nv_bfloat162 w = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&w);
+  };
+  for (int u = threadIdx.x; u < ROPE_TOKENS * units; u += ROPE_THREADS) {
+    const int tt = u / units, w = u - tt * units;
+    const int slot = s_slot[tt];
+    if (slot < 0) continue;
+    const int hh = w >> 3, c = (w & 7) * 8;
+    const long long t = t0 + tt;
+    const TIn* src;
+    __nv_bfloat16* dst;
+    if (hh < Hq) {
+      src = q + (t * Hq + hh) * PG_D;
+      dst = q_rot + (t * Hq + hh) * PG_D;
+    } else {
+      const bool is_v = hh >= Hq + Hkv;
+      const int h = hh - Hq - (is_v ? Hkv : 0);
+      src = (is_v ? v : k) + (t * Hkv + h) * PG_D;
+      dst = (is_v ? v_pages : k_pages) + (((long long)(slot / P) * Hkv + h) * P + slot % P) * PG_D;
+    }
+    float a[8], b[8];
+    RowLoader<TIn>::load(src + c, a);
+    RowLoader<TIn>::load(src + c + HALF, b);
+    if (hh < Hq + Hkv) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float co = s_cos[tt][c + j], si = s_sin[tt][c + j], x1 = a[j], x2 = b[j];
+        a[j] = __fsub_rn(__fmul_rn(x1, co), __fmul_rn(x2, si));
+        b[j] = __fadd_rn(__fmul_rn(x2, co), __fmul_rn(x1, si));
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + c) = make_uint4(pack(a[0], a[1]), pack(a[2], a[3]), pack(a[4], a[5]), pack(a[6], a[7]));
+    *reinterpret_cast<uint4*>(dst + c + HALF) =
+        make_uint4(pack(b[0], b[1]), pack(b[2], b[3]), pack(b[4], b[5]), pack(b[6], b[7]));
+  }
+}
+
+}  // namespace bitnet

@@ -9,7 +9,15 @@
 // One CTA per token.  The row is staged once in shared memory as fp32; the three
 // reductions (max|x|, the fixed-point sum of x^2, max|y|) and the sum of q are exact,
 // so the result is independent of the thread count and of the order of summation.
+//
+// With a residual type TRes (bitnet_add_rmsnorm_quant_act) the kernels first add the residual
+// stream: r' = TRes(x + r), one fp32 addition and one rounding, is written to r_out and is what
+// the norm reads, so the codes are those of the plain kernels run on r'.  The row is in registers
+// or shared memory anyway, so the stream is read and written once and r' is not read again.
+// Every value is read before its own r_out is written, by the same thread: r_out may be r_in.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace bitnet {
@@ -43,6 +51,42 @@ struct RowLoader<float> {
   }
   BN_DEV static float load1(const float* p) { return *p; }
 };
+
+// v[0..8) = the stored residual TRes(v + r_in[0..8)).
+template <typename TRes>
+BN_DEV void add_residual8(float* v, const TRes* r_in, TRes* r_out) {
+  float r[8];
+  RowLoader<TRes>::load(r_in, r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __fadd_rn(v[i], r[i]);
+  if constexpr (std::is_same<TRes, float>::value) {
+    reinterpret_cast<float4*>(r_out)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(r_out)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+    *reinterpret_cast<uint4*>(r_out) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+// The same for one value.
+template <typename TRes>
+BN_DEV float add_residual1(float v, const TRes* r_in, TRes* r_out) {
+  v = __fadd_rn(v, RowLoader<TRes>::load1(r_in));
+  if constexpr (std::is_same<TRes, float>::value) {
+    *r_out = v;
+    return v;
+  } else {
+    const __nv_bfloat16 b = __float2bfloat16_rn(v);
+    *r_out = b;
+    return __bfloat162float(b);
+  }
+}
 
 // Quantise one staged row xs[0..K) in place of nothing: writes q, s_x, sum_q of the row.
 // `vec` says whether K % 8 == 0 and the row pointers are 16-byte aligned.
@@ -112,15 +156,17 @@ BN_DEV void quantise_staged_row(float* xs, int K, const float* gain, float eps, 
   }
 }
 
-// Stage row `x` [K] into xs as fp32; returns max|x| over the block.
-template <typename TIn>
-BN_DEV float stage_row(const TIn* x, int K, float* xs, bool vec, void* red_scratch) {
+// Stage row `x` [K] into xs as fp32 (with a residual type: the stored sum); returns max|x| over the block.
+template <typename TIn, typename TRes = void>
+BN_DEV float stage_row(const TIn* x, int K, float* xs, bool vec, void* red_scratch, const TRes* r_in = nullptr,
+                       TRes* r_out = nullptr) {
   const int tid = threadIdx.x, nt = blockDim.x;
   float am = 0.0f;
   if (vec) {
     for (int k = tid * 8; k < K; k += nt * 8) {
       float v[8];
       RowLoader<TIn>::load(x + k, v);
+      if constexpr (!std::is_void<TRes>::value) add_residual8<TRes>(v, r_in + k, r_out + k);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         xs[k + j] = v[j];
@@ -129,7 +175,8 @@ BN_DEV float stage_row(const TIn* x, int K, float* xs, bool vec, void* red_scrat
     }
   } else {
     for (int k = tid; k < K; k += nt) {
-      const float v = RowLoader<TIn>::load1(x + k);
+      float v = RowLoader<TIn>::load1(x + k);
+      if constexpr (!std::is_void<TRes>::value) v = add_residual1<TRes>(v, r_in + k, r_out + k);
       xs[k] = v;
       am = fmaxf(am, fabsf(v));
     }
@@ -137,17 +184,21 @@ BN_DEV float stage_row(const TIn* x, int K, float* xs, bool vec, void* red_scrat
   return block_reduce(am, reinterpret_cast<float*>(red_scratch), MaxOp());
 }
 
-template <typename TIn>
+template <typename TIn, typename TRes = void>
 __global__ void __launch_bounds__(1024) k_rmsnorm_quant(const TIn* __restrict__ x, const float* __restrict__ gain,
                                                         float eps, int K, int8_t* __restrict__ q,
                                                         float* __restrict__ s_x, int32_t* __restrict__ sum_q,
-                                                        int vec) {
+                                                        int vec, const TRes* r_in, TRes* r_out) {
   extern __shared__ float xs[];
   __shared__ long long red[32];
   const long long t = blockIdx.x;
   pdl_launch_dependents();
   pdl_wait();
-  const float amax = stage_row<TIn>(x + t * K, K, xs, vec != 0, red);
+  float amax;
+  if constexpr (std::is_void<TRes>::value)
+    amax = stage_row<TIn>(x + t * K, K, xs, vec != 0, red);
+  else
+    amax = stage_row<TIn, TRes>(x + t * K, K, xs, vec != 0, red, r_in + t * K, r_out + t * K);
   quantise_staged_row(xs, K, gain, eps, q + t * K, s_x + t, sum_q + t, vec != 0, red, amax);
 }
 
@@ -354,11 +405,12 @@ BN_DEV T qw_reduce(T v, T* slots, int& flip, int bar_id, int rank, Op op) {
   return r;
 }
 
-template <typename TIn, int W>
+template <typename TIn, int W, typename TRes = void>
 __global__ void __launch_bounds__(QW_THREADS) k_rmsnorm_quant_warps(const TIn* __restrict__ x,
                                                                    const float* __restrict__ gain, float eps, int T,
                                                                    int K, int8_t* __restrict__ q,
-                                                                   float* __restrict__ s_x, int32_t* __restrict__ sum_q) {
+                                                                   float* __restrict__ s_x, int32_t* __restrict__ sum_q,
+                                                                   const TRes* r_in, TRes* r_out) {
   constexpr int ROWS = QW_THREADS / 32 / W;
   __shared__ float redf[ROWS][2 * W];
   __shared__ long long redl[ROWS][2 * W];
@@ -379,6 +431,7 @@ __global__ void __launch_bounds__(QW_THREADS) k_rmsnorm_quant_warps(const TIn* _
     const int k = 8 * (lane + 32 * (rank + W * j));
     if (k < K) {
       RowLoader<TIn>::load(xr + k, v[j]);
+      if constexpr (!std::is_void<TRes>::value) add_residual8<TRes>(v[j], r_in + t * K + k, r_out + t * K + k);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
