@@ -327,6 +327,7 @@ bitnet_status bitnet_attention_decode(const float* q_rot, const void* k_cache, c
  * counterpart: the arithmetic is that of the single-sequence entries above, over a paged cache.) */
 #define BITNET_MAX_REQUESTS 4096
 #define BITNET_MAX_STEP_TOKENS (1 << 22)
+#define BITNET_MAX_KV_ROWS (1 << 30)
 
 /* Residual addition in front of bitnet_rmsnorm_quant_act:
  *   r' = x + residual (one fp32 addition, rounded to the residual's type rt)   -> residual_out
@@ -360,7 +361,7 @@ bitnet_status bitnet_add_rmsnorm_quant_act(const void* x, bitnet_dtype xt, const
  * BITNET_ERR_INDEX, as does an n_free outside [0, n_list].  T may exceed the tokens (padding of a
  * fixed-size step).
  * Errors: NULL, SHAPE (B > BITNET_MAX_REQUESTS, T > BITNET_MAX_STEP_TOKENS, page_size, or
- * width * page_size beyond int32), ALIGN. */
+ * width * page_size > BITNET_MAX_KV_ROWS), ALIGN. */
 bitnet_status bitnet_paged_plan(const int32_t* new_lens, const int32_t* ctx_lens, int64_t B, int64_t page_size,
                                 int32_t* block_table, int64_t width, const int32_t* free_pages, int64_t n_list,
                                 const int32_t* n_free, int64_t T, int32_t* cu_new, int32_t* kv_lens,

@@ -32,7 +32,6 @@ struct PagedArgs {
   int4* desc;                    // [C] what a CTA's first tile is, where it ends that tile
   float* part;                   // [C][2] partial tiles
   int T, B, Hq, Hkv, G, P, log2P, width, n_pages, max_new, out_dtype;
-  int rows_above, rows_upto;     // the requests of this launch: rows_above < new * G <= rows_upto
 };
 
 constexpr float PG_SCALE_LOG2 = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
@@ -70,19 +69,18 @@ struct PagedWalk {
   int head, tile, tiles;
   int unit;            // next unit of the tile
   long long pos;       // its place on the line
-  int left;            // units of this CTA still to do
-  int per;             // units per CTA
+  long long left;      // units of this CTA still to do
+  long long per;       // units per CTA
 
-  // Units of one request and head, or 0 if this launch does not take the request.
-  BN_DEV static int request_units(const PagedArgs& a, int i, bool& bad) {
+  // Units of one request and head, or 0 for a request whose lengths do not fit.
+  BN_DEV static long long request_units(const PagedArgs& a, int i, bool& bad) {
     int t0, n, kv;
     if (!paged_request(a, i, t0, n, kv)) {
       bad = true;
       return 0;
     }
     const int R = n * a.G;
-    if (R <= a.rows_above || R > a.rows_upto) return 0;
-    int w = 0;
+    long long w = 0;
     for (int j = 0; j * M < R; ++j) w += tile_units<M, U>(n, kv, a.G, j);
     return w;
   }
@@ -98,14 +96,14 @@ struct PagedWalk {
     if (threadIdx.x == 0) sm[0] = -1;
     __syncthreads();
     const long long share = (total + C - 1) / C;
-    per = (int)share;
+    per = share;
     pos = (long long)blockIdx.x * share;
-    left = (int)max(0ll, min(share, total - pos));
+    left = max(0ll, min(share, total - pos));
     if (left == 0) return;
     long long before = 0;
     for (int i0 = 0; i0 < a.B; i0 += blockDim.x) {
       const int i = i0 + threadIdx.x;
-      const long long w = i < a.B ? (long long)request_units(a, i, bad) * a.Hkv : 0;
+      const long long w = i < a.B ? request_units(a, i, bad) * a.Hkv : 0;
       long long v = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -131,11 +129,11 @@ struct PagedWalk {
     }
     seq = (int)sm[0];
     const long long off = sm[1];
-    const int w = (int)sm[2];
+    const long long w = sm[2];
     paged_request(a, seq, t0, n, kv);
     tiles = (n * a.G + M - 1) / M;
     head = (int)(off / w);
-    int rem = (int)(off - (long long)head * w);
+    long long rem = off - head * w;
     tile = 0;
     for (;;) {
       const int u = tile_units<M, U>(n, kv, a.G, tile);
@@ -143,7 +141,7 @@ struct PagedWalk {
       rem -= u;
       ++tile;
     }
-    unit = rem;
+    unit = (int)rem;
   }
 
   BN_DEV int units(const PagedArgs& a) const { return tile_units<M, U>(n, kv, a.G, tile); }
@@ -159,12 +157,9 @@ struct PagedWalk {
     tile = 0;
     if (++head < a.Hkv) return;
     head = 0;
-    for (;;) {  // units are left, so a request of this launch follows
+    do {  // units are left, so a request with tokens follows
       ++seq;
-      if (!paged_request(a, seq, t0, n, kv)) continue;
-      const int R = n * a.G;
-      if (R > a.rows_above && R <= a.rows_upto) break;
-    }
+    } while (!paged_request(a, seq, t0, n, kv) || n == 0);
     tiles = (n * a.G + M - 1) / M;
   }
 };
@@ -238,7 +233,7 @@ __global__ void __launch_bounds__(PD_THREADS, 2) k_attn_paged_few(const PagedArg
 
   while (w.left > 0) {
     const int nu = w.units(a);
-    const int cnt = min(w.left, nu - w.unit);
+    const int cnt = (int)min(w.left, (long long)(nu - w.unit));
     const int R = w.n * a.G, r0 = w.tile * PD_M;
     const int vis = tile_visible<PD_M>(w.n, w.kv, a.G, w.tile);
     // this thread's two query rows (g and g + 8 of the tile): what they see, and their q fragments

@@ -20,6 +20,7 @@
 #include "attention.cuh"
 #include "paged.cuh"
 #include "attn_paged.cuh"
+#include "attn_chunk.cuh"
 
 namespace bitnet {
 
@@ -1262,7 +1263,7 @@ bitnet_status bitnet_paged_plan(const int32_t* new_lens, const int32_t* ctx_lens
                                 const int32_t* n_free, int64_t T, int32_t* cu_new, int32_t* kv_lens,
                                 int32_t* positions, int32_t* slots, int32_t* n_free_out, bitnet_stream stream) {
   if (B < 0 || B > BITNET_MAX_REQUESTS || T < 0 || T > BITNET_MAX_STEP_TOKENS || page_log2(page_size) < 0 ||
-      width <= 0 || width * page_size > 0x7FFFFFFFll || n_list < 0 || n_list > 0x7FFFFFFFll)
+      width <= 0 || width * page_size > BITNET_MAX_KV_ROWS || n_list < 0 || n_list > 0x7FFFFFFFll)
     return BITNET_ERR_SHAPE;
   if (!cu_new || !n_free || !n_free_out || (B > 0 && (!new_lens || !ctx_lens || !block_table || !kv_lens)) ||
       (n_list > 0 && !free_pages) || (T > 0 && (!positions || !slots)))
@@ -1311,13 +1312,32 @@ bitnet_status bitnet_rope_paged_append(const void* q, const void* k, const void*
   return e == cudaSuccess ? BITNET_OK : cuda_fail(e, "k_rope_paged");
 }
 
-// The workspace: the few-row launch's tile descriptors (16 bytes per CTA) and partial tiles.
-static int paged_few_ctas() { return 2 * device_sm_count(); }
+// bf16 pages [n_pages][Hkv][P][128], box of 64 columns and min(P, 128) rows of one page and head.
+static bool make_map_pages(CUtensorMap* m, const void* base, int64_t n_pages, int64_t Hkv, int64_t P) {
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {PG_D, (cuuint64_t)P, (cuuint64_t)Hkv, (cuuint64_t)n_pages};
+  const cuuint64_t strides[3] = {PG_D * 2, (cuuint64_t)P * PG_D * 2, (cuuint64_t)(Hkv * P) * PG_D * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(P < 128 ? P : 128), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Which kernel a call takes: up to PAGED_FEW_ROWS query rows per request and key/value head the
+// mma.sync one, which reads the cache once per 16 rows, above them the tcgen05 one.
+constexpr int64_t PAGED_FEW_ROWS = 64;
+static bool paged_few(int64_t G, int64_t max_new) { return max_new * G <= PAGED_FEW_ROWS; }
+static int paged_ctas(bool few) { return (few ? 2 : 1) * device_sm_count(); }
+
+// The workspace: tile descriptors (16 bytes per CTA) and two partial tiles per CTA.
 
 size_t bitnet_attention_paged_workspace_bytes(int64_t Hq, int64_t Hkv, int64_t max_new) {
   if (Hq <= 0 || Hkv <= 0 || Hq > 1024 || Hq % Hkv || max_new < 0) return 0;
-  const size_t few = (size_t)paged_few_ctas();
-  return align_up(few * 16) + align_up(few * 2 * PD_PART * 4);
+  const bool few = paged_few(Hq / Hkv, max_new);
+  const size_t ctas = (size_t)paged_ctas(few);
+  return align_up(ctas * 16) + align_up(ctas * 2 * (few ? PD_PART : PC_PART) * 4);
 }
 
 bitnet_status bitnet_attention_paged(const void* q_rot, const void* k_pages, const void* v_pages,
@@ -1329,7 +1349,7 @@ bitnet_status bitnet_attention_paged(const void* q_rot, const void* k_pages, con
   const int log2P = page_log2(page_size);
   if (T < 0 || T > BITNET_MAX_STEP_TOKENS || B < 0 || B > BITNET_MAX_REQUESTS || Hq <= 0 || Hkv <= 0 || Hq > 1024 ||
       Hq % Hkv || d != PG_D || log2P < 0 || n_pages <= 0 || n_pages * page_size > 0x7FFFFFFFll || width <= 0 ||
-      width * page_size > 0x7FFFFFFFll || max_new < 0)
+      width * page_size > BITNET_MAX_KV_ROWS || max_new < 0)
     return BITNET_ERR_SHAPE;
   if (T == 0 || B == 0 || max_new == 0) return BITNET_OK;
   if (!q_rot || !k_pages || !v_pages || !block_table || !cu_new || !kv_lens || !out) return BITNET_ERR_NULL;
@@ -1359,17 +1379,29 @@ bitnet_status bitnet_attention_paged(const void* q_rot, const void* k_pages, con
   a.max_new = (int)(max_new < T ? max_new : T);
   a.out_dtype = ot;
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
-  const int few = paged_few_ctas();
+  const bool few = paged_few(a.G, max_new);
+  const int ctas = paged_ctas(few);
   a.desc = reinterpret_cast<int4*>(w);
-  a.part = reinterpret_cast<float*>(w + align_up((size_t)few * 16));
-  a.rows_above = 0;
-  a.rows_upto = 0x7FFFFFFF;
-  cudaError_t e = opt_in_smem((const void*)k_attn_paged_few, 8);
-  if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_few attribute");
-  e = launch(k_attn_paged_few, dim3((unsigned)few), dim3(PD_THREADS), PD_RING, s, true, a);
-  if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_few");
-  e = launch(k_attn_paged_few_join, dim3((unsigned)few), dim3(256), 0, s, true, a);
-  if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_few_join");
+  a.part = reinterpret_cast<float*>(w + align_up((size_t)ctas * 16));
+  cudaError_t e;
+  if (few) {
+    e = opt_in_smem((const void*)k_attn_paged_few, 14);
+    if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_few attribute");
+    e = launch(k_attn_paged_few, dim3((unsigned)ctas), dim3(PD_THREADS), PD_RING, s, true, a);
+    if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_few");
+    e = launch(k_attn_paged_few_join, dim3((unsigned)ctas), dim3(256), 0, s, true, a);
+    if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_few_join");
+    return BITNET_OK;
+  }
+  PagedMaps maps;
+  if (!make_map_pages(&maps.k, k_pages, n_pages, Hkv, page_size) || !make_map_pages(&maps.v, v_pages, n_pages, Hkv, page_size))
+    return cuda_fail(cudaErrorUnknown, "cuTensorMapEncodeTiled (pages)");
+  e = opt_in_smem((const void*)k_attn_paged_chunk, 15);
+  if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_chunk attribute");
+  e = launch(k_attn_paged_chunk, dim3((unsigned)ctas), dim3(PC_THREADS), PC_SMEM, s, true, maps, a);
+  if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_chunk");
+  e = launch(k_attn_paged_chunk_join, dim3((unsigned)ctas, PG_D / 16), dim3(PC_M), 0, s, true, a);
+  if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_chunk_join");
   return BITNET_OK;
 }
 
