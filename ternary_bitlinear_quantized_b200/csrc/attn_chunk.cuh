@@ -5,7 +5,7 @@
 //                   tensor memory, maximum, weights (bf16) back to tensor memory; the output at the end
 //   warp 8          tcgen05.mma: S = Q K^T (both operands in shared memory), O += P V (P in tensor memory)
 //   warp 9          TMA loads of K and V, page by page, into a ring of 32 KB slots
-//   warp 10         cp.async loads of the next tile's Q (rows of any group size, so not a box)
+//   warp 10         TMA loads of the next tile's Q
 // The two halves take turns: while one half's softmax runs, the tensor core does the other's
 // products.  Tensor memory (512 columns): S of each half 128 columns, of which P takes the first 64
 // once the scores are in registers; O of each half 128 columns.
@@ -27,11 +27,38 @@
 
 namespace bitnet {
 
-constexpr int PC_M = 256;
-constexpr int PC_U = 128;
+// A block of at most 128 query rows is TB tokens of GB query heads, row = token * GB + head, so that
+// one box of q holds it: GB = min(G, 128), TB = 128 / GB; NB = ceil(G / 128) blocks cover a token's
+// heads.  A tile is two consecutive blocks of a request and key/value head.
+struct ChunkTiles {
+  static constexpr int M = 256, U = 128;
+  BN_DEV static int blocks(const PagedArgs& a, int n) { return (n + a.TB - 1) / a.TB * a.NB; }
+  BN_DEV static int tiles(const PagedArgs& a, int n) { return (blocks(a, n) + 1) >> 1; }
+  BN_DEV static int visible(const PagedArgs& a, int n, int kv, int j) {
+    const int b = 2 * j + 1, group = a.NB == 1 ? b : b / a.NB;
+    return max(0, kv - n + min(n, (group + 1) * a.TB));
+  }
+};
+// A row of a tile: its token and head (of the G), and whether the request has it.
+struct ChunkRow {
+  int t, g;
+  bool there;
+};
+BN_DEV ChunkRow chunk_row(const PagedArgs& a, int n, int tile, int row) {
+  const int b = 2 * tile + (row >> 7), i = row & 127, ti = i / a.GB;
+  ChunkRow r;
+  r.t = (a.NB == 1 ? b : b / a.NB) * a.TB + ti;
+  r.g = (a.NB == 1 ? 0 : (b % a.NB) * 128) + i - ti * a.GB;
+  r.there = ti < a.TB && r.t < n && r.g < a.G;
+  return r;
+}
+
+constexpr int PC_M = ChunkTiles::M;
+constexpr int PC_U = ChunkTiles::U;
 constexpr int PC_THREADS = 384;
 constexpr int PC_MMA_WARP = 8, PC_KV_WARP = 9, PC_Q_WARP = 10;
 constexpr int PC_SLOTS = 5;
+constexpr int PC_EARLY = 96;  // weights that the second product starts with, while the others are computed
 constexpr uint32_t PC_TILE_BYTES = 128 * 256;  // 128 rows of 128 bf16: two 64-column halves of 128-byte rows, swizzled
 constexpr int PC_SMEM = (2 + PC_SLOTS) * PC_TILE_BYTES + 1024;
 constexpr int PC_PART = PC_M * (PG_D + 2);     // floats of a partial tile: values [32][256 rows][4], maxima, sums
@@ -39,6 +66,7 @@ constexpr float PC_GROW = 8.0f / PG_SCALE_LOG2;
 
 struct alignas(64) PagedMaps {
   CUtensorMap k, v;  // bf16 [n_pages][Hkv][P][128], box {64, min(P, 128), 1, 1}, 128-byte swizzle
+  CUtensorMap q;     // bf16 [T][Hkv][G][128], box {64, GB, 1, TB}, the same
 };
 
 // bf16 x bf16 -> fp32, M = N = 128; `mn_b`: B is stored with its N index contiguous
@@ -122,10 +150,10 @@ BN_DEV bool warp_wait(uint32_t bar, uint32_t parity) { return __all_sync(0xfffff
 
 __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid_constant__ PagedMaps maps, const PagedArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) unsigned long long s_bars[2 * PC_SLOTS + 7];
+  __shared__ __align__(8) unsigned long long s_bars[2 * PC_SLOTS + 9];
   __shared__ long long s_walk[4], s_red[32];
   volatile __shared__ int s_abort;
-  __shared__ int s_issued;  // ring slots that the producer filled (for the drain after an abort)
+  __shared__ int s_issued, s_q_issued;  // ring slots and tiles of Q that were loaded (for the drain after an abort)
   __shared__ uint32_t s_tmem;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -136,7 +164,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
   const uint32_t bar0 = bars + 8u * 2 * PC_SLOTS;
   const uint32_t q_full = bar0, q_empty = bar0 + 8, mma_done = bar0 + 16;
   auto s_full = [&](int w) { return bar0 + 24u + 8u * w; };
-  auto p_full = [&](int w) { return bar0 + 40u + 8u * w; };
+  auto p_full = [&](int w, int part) { return bar0 + 40u + 8u * (2 * w + part); };
   if (threadIdx.x == 0) {
     for (int s = 0; s < PC_SLOTS; ++s) {
       mbar_init(full(s), 1);
@@ -147,10 +175,12 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
     mbar_init(mma_done, 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(s_full(w), 1);
-      mbar_init(p_full(w), 4);
+      mbar_init(p_full(w, 0), 4);
+      mbar_init(p_full(w, 1), 4);
     }
     s_abort = 0;
     s_issued = 0;
+    s_q_issued = 0;
     fence_mbar_init();
   }
   if (warp == PC_MMA_WARP) {
@@ -163,7 +193,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
   const uint32_t tmem = s_tmem;
   pdl_launch_dependents();
   pdl_wait();
-  PagedWalk<PC_M, PC_U> w;
+  PagedWalk<ChunkTiles> w;
   w.begin(a, gridDim.x, s_walk, s_red);
   if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
@@ -183,11 +213,9 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
     bool ok = true;
     while (w.left > 0 && ok) {
       const int nu = w.units(a), cnt = (int)min(w.left, (long long)(nu - w.unit));
-      const int R = w.n * a.G, r = w.tile * PC_M + row;
-      if (w.tile * PC_M + half * 128 < R) {
-        const bool there = r < R;
-        const int t = there ? r / a.G : 0;
-        const int lim = there ? max(0, w.kv - w.n + t + 1) : 0x7FFFFFFF;  // rows of the cache that this row sees
+      if (2 * w.tile + half < ChunkTiles::blocks(a, w.n)) {
+        const ChunkRow r = chunk_row(a, w.n, w.tile, row);
+        const int lim = r.there ? max(0, w.kv - w.n + r.t + 1) : 0x7FFFFFFF;  // rows of the cache that this row sees
         float m = -INFINITY, l = 0.0f;  // running maximum of the raw scores (may trail by 2^8), sum
         for (int it = 0; it < cnt; ++it) {
           ok = warp_wait(s_full(half), ph) && !s_abort;
@@ -249,11 +277,13 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
               p[k >> 1] = pack_bf16(x, y);
             }
             tmem_st16(tS + (c >> 1), p);
+            if (c >= PC_EARLY - 32) {
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0 && (c == PC_EARLY - 32 || c == 96)) mbar_arrive(p_full(half, c == 96));
+            }
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full(half));
           float x, y;
           unpack_f32x2(add_f32x2(sum2[0], sum2[1]), x, y);
           l = __fadd_rn(l, __fadd_rn(x, y));
@@ -266,13 +296,13 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
         tc_fence_after();
         if (cnt == nu) {
           const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);  // NaN stays
-          const long long off = ((long long)(w.t0 + t) * a.Hq + w.head * a.G + (r - t * a.G)) * PG_D;
+          const long long off = ((long long)(w.t0 + r.t) * a.Hq + w.head * a.G + r.g) * PG_D;
 #pragma unroll 1
           for (int c = 0; c < 128; c += 32) {
             float o[32];
             tmem_ld32(tO + c, o);
             tmem_wait_ld();
-            if (!there) continue;
+            if (!r.there) continue;
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = l == 0.0f ? 0.0f : __fmul_rn(o[k], inv);
             if (a.out_dtype == BITNET_BF16) {
@@ -326,15 +356,15 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
                      kk > 0);
       }
     };
-    auto values = [&](int h, uint32_t v_addr, bool first) {
+    auto values = [&](int h, uint32_t v_addr, bool first, int k0, int k1) {
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
+      for (int kk = k0; kk < k1; ++kk)
         umma_bf16_ts(tmem + 256 + h * 128, tmem + h * 128 + kk * 8, pc_desc_v(v_addr + kk * 2048), pc_idesc(true),
                      (first && kk == 0) ? 0u : 1u);
     };
     while (w.left > 0 && ok && !s_abort) {
       const int nu = w.units(a), cnt = (int)min(w.left, (long long)(nu - w.unit));
-      const int nh = w.tile * PC_M + 128 < w.n * a.G ? 2 : 1;
+      const int nh = 2 * w.tile + 1 < ChunkTiles::blocks(a, w.n) ? 2 : 1;
       ok = warp_wait(q_full, ph_q) && warp_wait(full(slot), ph_s);
       if (!ok) break;
       ph_q ^= 1u;
@@ -370,12 +400,17 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
         }
         for (int h = 0; h < nh; ++h) {
           if (h == 0 && it + 1 < cnt) ok = warp_wait(full(slot), ph_s);
-          ok = ok && warp_wait(p_full(h), ph_p[h]);
+          ok = ok && warp_wait(p_full(h, 0), ph_p[h]);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) values(h, v, it == 0, 0, PC_EARLY / 16);
+          __syncwarp();
+          ok = warp_wait(p_full(h, 1), ph_p[h]);
           if (!ok) break;
           ph_p[h] ^= 1u;
           tc_fence_after();
           if (lane == 0) {
-            values(h, v, it == 0);
+            values(h, v, false, PC_EARLY / 16, 8);
             if (it + 1 < cnt) scores(h, ring + slot * PC_TILE_BYTES);
             if (h == nh - 1) {
               umma_commit(empty(vs));
@@ -399,7 +434,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
     bool ok = true;
     while (w.left > 0 && ok && !s_abort) {
       const int nu = w.units(a), cnt = (int)min(w.left, (long long)(nu - w.unit));
-      const int vis = tile_visible<PC_M>(w.n, w.kv, a.G, w.tile);
+      const int vis = ChunkTiles::visible(a, w.n, w.kv, w.tile);
       const int* trow = a.table + (long long)w.seq * a.width;
       // this lane's page of a unit: its id, or n_pages (zeros) where there is none to see
       auto page_of = [&](int u) {
@@ -447,18 +482,18 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
       ok = warp_wait(q_empty, ph);
       if (!ok) break;
       ph ^= 1u;
-      const int R = w.n * a.G, r0 = w.tile * PC_M, ch = lane & 15;
-      for (int i = lane >> 4; i < PC_M; i += 2) {
-        const int r = r0 + i, t = r / a.G;
-        const bool there = r < R;
-        const long long off = there ? ((long long)(w.t0 + t) * a.Hq + w.head * a.G + (r - t * a.G)) * PG_D + ch * 8 : 0;
-        cp_async16_or_zero(sQ + (i >> 7) * PC_TILE_BYTES + (ch >> 3) * 16384 + (i & 127) * 128 + (((ch & 7) ^ (i & 7)) << 4), a.q + off,
-                           there);
+      if (lane == 0) {
+        const int nh = 2 * w.tile + 1 < ChunkTiles::blocks(a, w.n) ? 2 : 1;
+        mbar_arrive_expect_tx(q_full, nh * a.TB * a.GB * PG_D * 2);
+        for (int h = 0; h < nh; ++h) {
+          const ChunkRow r = chunk_row(a, w.n, w.tile, h * 128);
+          const uint32_t dst = sQ + h * PC_TILE_BYTES;
+          tma_load_4d(dst, &maps.q, 0, r.g, w.head, w.t0 + r.t, q_full);
+          tma_load_4d(dst + 16384, &maps.q, 64, r.g, w.head, w.t0 + r.t, q_full);
+        }
+        ++s_q_issued;
       }
-      cp_async_wait_all();
-      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
       w.advance(a, cnt, nu);
     }
     if (!ok) s_abort = 1;
@@ -473,6 +508,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
       umma_commit(mma_done);
       mbar_drain(mma_done, 0);
     }
+    if (warp == PC_Q_WARP && lane == 0 && s_q_issued > 0) mbar_drain(q_full, (uint32_t)((s_q_issued - 1) & 1));
     if (warp == PC_KV_WARP && lane == 0)
       for (int k = max(0, s_issued - PC_SLOTS); k < s_issued; ++k) mbar_drain(full(k % PC_SLOTS), (uint32_t)((k / PC_SLOTS) & 1));
   }
@@ -494,8 +530,8 @@ __global__ void __launch_bounds__(PC_M) k_attn_paged_chunk_join(const PagedArgs 
   int t0, n, kv;
   paged_request(a, d.y, t0, n, kv);
   const int row = threadIdx.x, g0 = blockIdx.y * 4;
-  const int r = d.w * PC_M + row;
-  if (r >= n * a.G) return;
+  const ChunkRow r = chunk_row(a, n, d.w, row);
+  if (!r.there) return;
   auto part = [&](int i) { return a.part + ((long long)i * 2 + (i == d.x ? 1 : 0)) * PC_PART; };
   float m = -INFINITY;
   for (int i = d.x; i <= c; ++i) m = fmaxf(m, part(i)[PC_M * PG_D + row]);
@@ -517,8 +553,7 @@ __global__ void __launch_bounds__(PC_M) k_attn_paged_chunk_join(const PagedArgs 
     }
   }
   const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);
-  const int t = r / a.G;
-  const long long off = ((long long)(t0 + t) * a.Hq + d.z * a.G + (r - t * a.G)) * PG_D + g0 * 4;
+  const long long off = ((long long)(t0 + r.t) * a.Hq + d.z * a.G + r.g) * PG_D + g0 * 4;
 #pragma unroll
   for (int k = 0; k < 16; ++k) o[k] = __fmul_rn(o[k], inv);
   if (a.out_dtype == BITNET_BF16) {

@@ -32,6 +32,7 @@ struct PagedArgs {
   int4* desc;                    // [C] what a CTA's first tile is, where it ends that tile
   float* part;                   // [C][2] partial tiles
   int T, B, Hq, Hkv, G, P, log2P, width, n_pages, max_new, out_dtype;
+  int TB, GB, NB;                // chunk kernel: a block of query rows is TB tokens x GB heads, NB blocks cover the G heads
 };
 
 constexpr float PG_SCALE_LOG2 = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
@@ -51,19 +52,23 @@ BN_DEV bool paged_request(const PagedArgs& a, int i, int& t0, int& n, int& kv) {
   return t0 >= 0 && t1 >= t0 && t1 <= a.T && n <= a.max_new && kv >= 0 && kv <= (long long)a.width * a.P;
 }
 
-// Cache rows that the last row of tile j sees (0 where it sees none).
-template <int M>
-BN_DEV int tile_visible(int n, int kv, int G, int j) {
-  const int last = min((j + 1) * M, n * G) - 1;
-  return max(0, kv - n + last / G + 1);
-}
-template <int M, int U>
-BN_DEV int tile_units(int n, int kv, int G, int j) {
-  return max(1, (tile_visible<M>(n, kv, G, j) + U - 1) / U);
+// How a kernel cuts a request's query rows (of one key/value head) into tiles, and how many cache
+// rows the last row of tile j sees (0 where it sees none).
+struct FewTiles {  // 16 consecutive rows
+  static constexpr int M = 16, U = 64;
+  BN_DEV static int tiles(const PagedArgs& a, int n) { return (n * a.G + M - 1) / M; }
+  BN_DEV static int visible(const PagedArgs& a, int n, int kv, int j) {
+    const int last = min((j + 1) * M, n * a.G) - 1;
+    return max(0, kv - n + last / a.G + 1);
+  }
+};
+template <typename Tiles>
+BN_DEV int tile_units(const PagedArgs& a, int n, int kv, int j) {
+  return max(1, (Tiles::visible(a, n, kv, j) + Tiles::U - 1) / Tiles::U);
 }
 
 // A CTA's place on the line of units.
-template <int M, int U>
+template <typename Tiles>
 struct PagedWalk {
   int seq, t0, n, kv;  // request
   int head, tile, tiles;
@@ -79,9 +84,9 @@ struct PagedWalk {
       bad = true;
       return 0;
     }
-    const int R = n * a.G;
+    const int k = Tiles::tiles(a, n);
     long long w = 0;
-    for (int j = 0; j * M < R; ++j) w += tile_units<M, U>(n, kv, a.G, j);
+    for (int j = 0; j < k; ++j) w += tile_units<Tiles>(a, n, kv, j);
     return w;
   }
 
@@ -89,8 +94,9 @@ struct PagedWalk {
   BN_DEV void begin(const PagedArgs& a, int C, long long* sm, long long* red) {
     bool bad = false;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    long long mine = 0;
-    for (int i = threadIdx.x; i < a.B; i += blockDim.x) mine += request_units(a, i, bad);
+    const long long first = threadIdx.x < a.B ? request_units(a, threadIdx.x, bad) : 0;
+    long long mine = first;
+    for (int i = threadIdx.x + blockDim.x; i < a.B; i += blockDim.x) mine += request_units(a, i, bad);
     const long long total = block_reduce(mine, red, AddOpLL()) * a.Hkv;
     if (bad && blockIdx.x == 0) flag_index_error();
     if (threadIdx.x == 0) sm[0] = -1;
@@ -103,7 +109,7 @@ struct PagedWalk {
     long long before = 0;
     for (int i0 = 0; i0 < a.B; i0 += blockDim.x) {
       const int i = i0 + threadIdx.x;
-      const long long w = i < a.B ? request_units(a, i, bad) * a.Hkv : 0;
+      const long long w = (i0 == 0 ? first : (i < a.B ? request_units(a, i, bad) : 0)) * a.Hkv;
       long long v = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -131,12 +137,12 @@ struct PagedWalk {
     const long long off = sm[1];
     const long long w = sm[2];
     paged_request(a, seq, t0, n, kv);
-    tiles = (n * a.G + M - 1) / M;
+    tiles = Tiles::tiles(a, n);
     head = (int)(off / w);
     long long rem = off - head * w;
     tile = 0;
     for (;;) {
-      const int u = tile_units<M, U>(n, kv, a.G, tile);
+      const int u = tile_units<Tiles>(a, n, kv, tile);
       if (rem < u) break;
       rem -= u;
       ++tile;
@@ -144,7 +150,7 @@ struct PagedWalk {
     unit = (int)rem;
   }
 
-  BN_DEV int units(const PagedArgs& a) const { return tile_units<M, U>(n, kv, a.G, tile); }
+  BN_DEV int units(const PagedArgs& a) const { return tile_units<Tiles>(a, n, kv, tile); }
 
   // Goes on behind `cnt` units of the tile.
   BN_DEV void advance(const PagedArgs& a, int cnt, int tile_total) {
@@ -160,7 +166,7 @@ struct PagedWalk {
     do {  // units are left, so a request with tokens follows
       ++seq;
     } while (!paged_request(a, seq, t0, n, kv) || n == 0);
-    tiles = (n * a.G + M - 1) / M;
+    tiles = Tiles::tiles(a, n);
   }
 };
 
@@ -178,8 +184,8 @@ struct PagedWalk {
 // Products are m16n8k16 bf16 with fp32 sums; the probabilities enter the second product as the
 // sum of two bf16 (p rounded, and what that left over), so their rounding is 2^-17 of p; the
 // extra instruction is free beside the read.
-constexpr int PD_M = 16;
-constexpr int PD_U = 64;
+constexpr int PD_M = FewTiles::M;
+constexpr int PD_U = FewTiles::U;
 constexpr int PD_WARPS = 4;
 constexpr int PD_THREADS = 32 * PD_WARPS;
 constexpr int PD_STAGES = 3;
@@ -224,7 +230,7 @@ __global__ void __launch_bounds__(PD_THREADS, 2) k_attn_paged_few(const PagedArg
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait();
-  PagedWalk<PD_M, PD_U> w;
+  PagedWalk<FewTiles> w;
   w.begin(a, gridDim.x, s_walk, s_red);
   if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
   const uint32_t ring = smem_addr(pd_sm) + warp * PD_STAGES * PD_STAGE_BYTES;
@@ -235,7 +241,7 @@ __global__ void __launch_bounds__(PD_THREADS, 2) k_attn_paged_few(const PagedArg
     const int nu = w.units(a);
     const int cnt = (int)min(w.left, (long long)(nu - w.unit));
     const int R = w.n * a.G, r0 = w.tile * PD_M;
-    const int vis = tile_visible<PD_M>(w.n, w.kv, a.G, w.tile);
+    const int vis = FewTiles::visible(a, w.n, w.kv, w.tile);
     // this thread's two query rows (g and g + 8 of the tile): what they see, and their q fragments
     int lim[2];
     uint32_t qf[8][4];

@@ -1312,13 +1312,13 @@ bitnet_status bitnet_rope_paged_append(const void* q, const void* k, const void*
   return e == cudaSuccess ? BITNET_OK : cuda_fail(e, "k_rope_paged");
 }
 
-// bf16 pages [n_pages][Hkv][P][128], box of 64 columns and min(P, 128) rows of one page and head.
-static bool make_map_pages(CUtensorMap* m, const void* base, int64_t n_pages, int64_t Hkv, int64_t P) {
+// bf16 [d3][d2][d1][128] (contiguous), box of 64 columns, b1 of d1, one of d2 and b3 of d3.
+static bool make_map_heads(CUtensorMap* m, const void* base, int64_t d1, int64_t d2, int64_t d3, int64_t b1, int64_t b3) {
   EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
-  const cuuint64_t dims[4] = {PG_D, (cuuint64_t)P, (cuuint64_t)Hkv, (cuuint64_t)n_pages};
-  const cuuint64_t strides[3] = {PG_D * 2, (cuuint64_t)P * PG_D * 2, (cuuint64_t)(Hkv * P) * PG_D * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)(P < 128 ? P : 128), 1, 1};
+  const cuuint64_t dims[4] = {PG_D, (cuuint64_t)d1, (cuuint64_t)d2, (cuuint64_t)d3};
+  const cuuint64_t strides[3] = {PG_D * 2, (cuuint64_t)d1 * PG_D * 2, (cuuint64_t)(d1 * d2) * PG_D * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)b1, 1, (cuuint32_t)b3};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1377,6 +1377,9 @@ bitnet_status bitnet_attention_paged(const void* q_rot, const void* k_pages, con
   a.width = (int)width;
   a.n_pages = (int)n_pages;
   a.max_new = (int)(max_new < T ? max_new : T);
+  a.GB = a.G < 128 ? a.G : 128;
+  a.TB = 128 / a.GB;
+  a.NB = (a.G + 127) / 128;
   a.out_dtype = ot;
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
   const bool few = paged_few(a.G, max_new);
@@ -1394,7 +1397,10 @@ bitnet_status bitnet_attention_paged(const void* q_rot, const void* k_pages, con
     return BITNET_OK;
   }
   PagedMaps maps;
-  if (!make_map_pages(&maps.k, k_pages, n_pages, Hkv, page_size) || !make_map_pages(&maps.v, v_pages, n_pages, Hkv, page_size))
+  const int64_t rows = page_size < 128 ? page_size : 128;
+  if (!make_map_heads(&maps.k, k_pages, page_size, Hkv, n_pages, rows, 1) ||
+      !make_map_heads(&maps.v, v_pages, page_size, Hkv, n_pages, rows, 1) ||
+      !make_map_heads(&maps.q, q_rot, a.G, Hkv, T, a.GB, a.TB))
     return cuda_fail(cudaErrorUnknown, "cuTensorMapEncodeTiled (pages)");
   e = opt_in_smem((const void*)k_attn_paged_chunk, 15);
   if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_chunk attribute");
