@@ -145,6 +145,14 @@ BN_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// One lane of a converged warp.  Unlike lane == 0 this tells the compiler that a single thread
+// follows, which lets it keep the operands of tcgen05.mma in uniform registers.
+BN_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P1;\n\telect.sync _|P1, 0xffffffff;\n\tselp.b32 %0, 1, 0, P1;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // The whole warp waits; false if any lane's wait ran out.
 BN_DEV bool warp_wait(uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity)); }
 
@@ -369,7 +377,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
       if (!ok) break;
       ph_q ^= 1u;
       tc_fence_after();
-      if (lane == 0) {
+      if (elect_one()) {
         const uint32_t k = ring + slot * PC_TILE_BYTES;
         for (int h = 0; h < nh; ++h) {
           scores(h, k);
@@ -403,13 +411,13 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
           ok = ok && warp_wait(p_full(h, 0), ph_p[h]);
           if (!ok) break;
           tc_fence_after();
-          if (lane == 0) values(h, v, it == 0, 0, PC_EARLY / 16);
+          if (elect_one()) values(h, v, it == 0, 0, PC_EARLY / 16);
           __syncwarp();
           ok = warp_wait(p_full(h, 1), ph_p[h]);
           if (!ok) break;
           ph_p[h] ^= 1u;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             values(h, v, false, PC_EARLY / 16, 8);
             if (it + 1 < cnt) scores(h, ring + slot * PC_TILE_BYTES);
             if (h == nh - 1) {
