@@ -3,9 +3,10 @@
 // of units with equal shares, one CTA per SM:
 //   warps 0-3, 4-7  softmax of the tile's rows 0-127 and 128-255, one thread per row: scores from
 //                   tensor memory, maximum, weights (bf16) back to tensor memory; the output at the end
-//   warp 8          tcgen05.mma: S = Q K^T (both operands in shared memory), O += P V (P in tensor memory)
-//   warp 9          TMA loads of K and V, page by page, into a ring of 32 KB slots
-//   warp 10         TMA loads of the next tile's Q
+//   warps 8, 9      one thread each, for the rows 0-127 and 128-255: tcgen05.mma S = Q K^T (both
+//                   operands in shared memory) and O += P V (P in tensor memory)
+//   warp 10         TMA loads of K, page by page, into a ring of three 32 KB slots, and of Q
+//   warp 11         TMA loads of V into a ring of two
 // The two halves take turns: while one half's softmax runs, the tensor core does the other's
 // products.  Tensor memory (512 columns): S of each half 128 columns, of which P takes the first 64
 // once the scores are in registers; O of each half 128 columns.
@@ -32,7 +33,7 @@ namespace bitnet {
 // heads.  A tile is two consecutive blocks of a request and key/value head.
 struct ChunkTiles {
   static constexpr int M = 256, U = 128;
-  BN_DEV static int blocks(const PagedArgs& a, int n) { return (n + a.TB - 1) / a.TB * a.NB; }
+  BN_DEV static int blocks(const PagedArgs& a, int n) { return div_small(n + a.TB - 1, a.by_TB) * a.NB; }
   BN_DEV static int tiles(const PagedArgs& a, int n) { return (blocks(a, n) + 1) >> 1; }
   BN_DEV static int visible(const PagedArgs& a, int n, int kv, int j) {
     const int b = 2 * j + 1, group = a.NB == 1 ? b : b / a.NB;
@@ -45,7 +46,7 @@ struct ChunkRow {
   bool there;
 };
 BN_DEV ChunkRow chunk_row(const PagedArgs& a, int n, int tile, int row) {
-  const int b = 2 * tile + (row >> 7), i = row & 127, ti = i / a.GB;
+  const int b = 2 * tile + (row >> 7), i = row & 127, ti = div_small(i, a.by_GB);
   ChunkRow r;
   r.t = (a.NB == 1 ? b : b / a.NB) * a.TB + ti;
   r.g = (a.NB == 1 ? 0 : (b % a.NB) * 128) + i - ti * a.GB;
@@ -56,11 +57,10 @@ BN_DEV ChunkRow chunk_row(const PagedArgs& a, int n, int tile, int row) {
 constexpr int PC_M = ChunkTiles::M;
 constexpr int PC_U = ChunkTiles::U;
 constexpr int PC_THREADS = 384;
-constexpr int PC_MMA_WARP = 8, PC_KV_WARP = 9, PC_Q_WARP = 10;
-constexpr int PC_SLOTS = 5;
-constexpr int PC_EARLY = 96;  // weights that the second product starts with, while the others are computed
+constexpr int PC_MMA_WARP = 8, PC_LOAD_WARP = 10;  // two warps each
+constexpr int PC_KSLOTS = 3, PC_VSLOTS = 2;
 constexpr uint32_t PC_TILE_BYTES = 128 * 256;  // 128 rows of 128 bf16: two 64-column halves of 128-byte rows, swizzled
-constexpr int PC_SMEM = (2 + PC_SLOTS) * PC_TILE_BYTES + 1024;
+constexpr int PC_SMEM = (2 + PC_KSLOTS + PC_VSLOTS) * PC_TILE_BYTES + 1024;
 constexpr int PC_PART = PC_M * (PG_D + 2);     // floats of a partial tile: values [32][256 rows][4], maxima, sums
 constexpr float PC_GROW = 8.0f / PG_SCALE_LOG2;
 
@@ -69,30 +69,34 @@ struct alignas(64) PagedMaps {
   CUtensorMap q;     // bf16 [T][Hkv][G][128], box {64, GB, 1, TB}, the same
 };
 
-// bf16 x bf16 -> fp32, M = N = 128; `mn_b`: B is stored with its N index contiguous
-BN_DEV constexpr uint32_t pc_idesc(bool mn_b) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((mn_b ? 1u : 0u) << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+// bf16 x bf16 -> fp32, M = 128; `mn_b`: B is stored with its N index contiguous
+BN_DEV constexpr uint32_t pc_idesc(int n, bool mn_b) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((mn_b ? 1u : 0u) << 16) | (((uint32_t)n >> 3) << 17) | ((128u >> 4) << 24);
 }
-// Descriptor of a V tile as B operand (d contiguous): 64-column halves 16384 bytes apart, groups of
-// eight cache rows 1024 bytes apart.
-BN_DEV uint64_t pc_desc_v(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(16384 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-BN_DEV void umma_bf16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// The upper words of the operands' descriptors (128-byte swizzle, eight-row groups 1024 bytes
+// apart); the lower word is the address / 16, with the distance of the 64-column halves (16384 bytes)
+// above it for V, whose d index is contiguous.
+constexpr uint32_t PC_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t PC_DESC_K = 1u << 16, PC_DESC_V = (16384u >> 4) << 16;
+// One tcgen05.mma.  The descriptors are put together inside the statement from a base and a constant
+// OFF (bytes / 16): as 64-bit operands the compiler keeps all of a loop's in registers, and spills them.
+template <uint32_t A_OFF, uint32_t B_OFF>
+BN_DEV void umma_bf16_ss(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\tadd.u32 x, %1, %4;\n\tadd.u32 y, %2, %5;\n\t"
+      "mov.b64 da, {x, %6};\n\tmov.b64 db, {y, %6};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %7, p;\n\t}"
+      ::"r"(d_tmem), "r"(a), "r"(b), "r"(accumulate), "n"(A_OFF), "n"(B_OFF), "r"(PC_DESC_HI), "r"(pc_idesc(64, false))
       : "memory");
 }
-BN_DEV void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+template <uint32_t B_OFF>
+BN_DEV void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b32 y;\n\t.reg .b64 db;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\tadd.u32 y, %2, %4;\n\tmov.b64 db, {y, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %6, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "r"(b), "r"(accumulate), "n"(B_OFF), "r"(PC_DESC_HI), "r"(pc_idesc(128, true))
       : "memory");
 }
 BN_DEV void tma_load_4d(uint32_t dst, const void* map, int x, int y, int z, int w, uint32_t bar) {
@@ -153,42 +157,72 @@ BN_DEV bool elect_one() {
   return p != 0;
 }
 
-// The whole warp waits; false if any lane's wait ran out.
-BN_DEV bool warp_wait(uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity)); }
+// The whole warp waits for a barrier that is most often ready; false (for all lanes) if a lane's
+// wait ran out or another warp gave up.
+BN_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity) && !*abort);
+}
+
+// Step B (cache rows 64 B .. 64 B + 63) of a unit for half h: S = Q K^T into columns 128 h + 64 B of
+// tensor memory (all 512 columns are allocated, so they begin at address 0), O (+)= P V into 256 + 128 h.
+template <int B, int KK = 0>
+BN_DEV void pc_scores(int h, uint32_t q, uint32_t k) {
+  constexpr uint32_t off = (KK >> 2) * 1024 + (KK & 3) * 2;
+  umma_bf16_ss<off, off + B * 512>(h * 128 + B * 64, q, k, KK > 0);
+  if constexpr (KK < 7) pc_scores<B, KK + 1>(h, q, k);
+}
+template <int B, int KK = 0>
+BN_DEV void pc_values(int h, uint32_t v, bool first) {
+  umma_bf16_ts<(B * 4 + KK) * 128>(256 + h * 128, h * 128 + B * 64 + KK * 8, v, !first);
+  if constexpr (KK < 3) pc_values<B, KK + 1>(h, v, false);
+}
+// First row of unit u behind kv if it lies inside a page of that unit (whose rows from there on may
+// hold anything), else 0.
+BN_DEV int pc_tail(const PagedArgs& a, int kv, int u) {
+  const int tail = kv - u * PC_U;
+  return tail > 0 && tail < PC_U && (tail & (a.P - 1)) ? tail : 0;
+}
 
 __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid_constant__ PagedMaps maps, const PagedArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) unsigned long long s_bars[2 * PC_SLOTS + 9];
-  __shared__ long long s_walk[4], s_red[32];
+  __shared__ __align__(8) unsigned long long s_bars[2 * PC_KSLOTS + 3 * PC_VSLOTS + 11];
+  __shared__ PagedWalkShared s_walk;
   volatile __shared__ int s_abort;
-  __shared__ int s_issued, s_q_issued;  // ring slots and tiles of Q that were loaded (for the drain after an abort)
+  __shared__ int s_issued[2], s_q_issued;  // tiles of K and V, and of Q, that were loaded (for the drain after an abort)
   __shared__ uint32_t s_tmem;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sQ = base, ring = base + 2 * PC_TILE_BYTES;
+  const uint32_t sQ = base, sK = base + 2 * PC_TILE_BYTES, sV = sK + PC_KSLOTS * PC_TILE_BYTES;
   const uint32_t bars = smem_addr(s_bars);
-  auto full = [&](int s) { return bars + 8u * s; };
-  auto empty = [&](int s) { return bars + 8u * (PC_SLOTS + s); };
-  const uint32_t bar0 = bars + 8u * 2 * PC_SLOTS;
+  auto k_full = [&](int s) { return bars + 8u * s; };
+  auto k_empty = [&](int s) { return bars + 8u * (PC_KSLOTS + s); };
+  auto v_full = [&](int s) { return bars + 8u * (2 * PC_KSLOTS + s); };
+  auto v_empty = [&](int s) { return bars + 8u * (2 * PC_KSLOTS + PC_VSLOTS + s); };
+  auto v_fixed = [&](int s) { return bars + 8u * (2 * PC_KSLOTS + 2 * PC_VSLOTS + s); };
+  const uint32_t bar0 = bars + 8u * (2 * PC_KSLOTS + 3 * PC_VSLOTS);
   const uint32_t q_full = bar0, q_empty = bar0 + 8, mma_done = bar0 + 16;
-  auto s_full = [&](int w) { return bar0 + 24u + 8u * w; };
-  auto p_full = [&](int w, int part) { return bar0 + 40u + 8u * (2 * w + part); };
+  auto s_full = [&](int h, int step) { return bar0 + 24u + 8u * (2 * h + step); };
+  auto p_full = [&](int h, int step) { return bar0 + 56u + 8u * (2 * h + step); };
   if (threadIdx.x == 0) {
-    for (int s = 0; s < PC_SLOTS; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
+    for (int s = 0; s < PC_KSLOTS; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 2);
+    }
+    for (int s = 0; s < PC_VSLOTS; ++s) {
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), 2);
+      mbar_init(v_fixed(s), 1);
     }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    mbar_init(mma_done, 1);
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(s_full(w), 1);
-      mbar_init(p_full(w, 0), 4);
-      mbar_init(p_full(w, 1), 4);
+    mbar_init(q_empty, 2);
+    mbar_init(mma_done, 2);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(s_full(i >> 1, i & 1), 1);
+      mbar_init(p_full(i >> 1, i & 1), 4);
     }
     s_abort = 0;
-    s_issued = 0;
-    s_q_issued = 0;
+    s_issued[0] = s_issued[1] = s_q_issued = 0;
     fence_mbar_init();
   }
   if (warp == PC_MMA_WARP) {
@@ -202,8 +236,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
   pdl_launch_dependents();
   pdl_wait();
   PagedWalk<ChunkTiles> w;
-  w.begin(a, gridDim.x, s_walk, s_red);
-  if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  w.begin(a, gridDim.x, &s_walk);
+  if (threadIdx.x == 0) a.desc[blockIdx.x].first = -1;
 
   // The launch gives every thread at most 168 registers (65536 / 384); the softmax warps, which hold a
   // row of scores, take 208: 8 * 32 * 208 + 4 * 32 * 80 <= 384 * 168 holds for the whole block.
@@ -217,90 +251,94 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
     const int half = warp >> 2, row = half * 128 + (warp & 3) * 32 + lane;
     const uint32_t t_lane = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + t_lane + half * 128, tO = tmem + t_lane + 256 + half * 128;
-    uint32_t ph = 0;
+    uint32_t ph = 0;  // parities of s_full, a bit per step
     bool ok = true;
     while (w.left > 0 && ok) {
       const int nu = w.units(a), cnt = (int)min(w.left, (long long)(nu - w.unit));
       if (2 * w.tile + half < ChunkTiles::blocks(a, w.n)) {
         const ChunkRow r = chunk_row(a, w.n, w.tile, row);
         const int lim = r.there ? max(0, w.kv - w.n + r.t + 1) : 0x7FFFFFFF;  // rows of the cache that this row sees
+        const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
         float m = -INFINITY, l = 0.0f;  // running maximum of the raw scores (may trail by 2^8), sum
-        for (int it = 0; it < cnt; ++it) {
-          ok = warp_wait(s_full(half), ph) && !s_abort;
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          ph ^= 1u;
-          tc_fence_after();
-          float s[128];
+        for (int it = 0; it < cnt && ok; ++it) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
-          tmem_wait_ld();
-          const int col0 = (w.unit + it) * PC_U;
-          if (__any_sync(0xffffffffu, lim < col0 + PC_U)) {
-            const int rel = lim - col0;
+          for (int b = 0; b < 2; ++b) {
+            ok = warp_wait(s_full(half, b), (ph >> b) & 1u, &s_abort);
+            if (!ok) break;
+            ph ^= 1u << b;
+            tc_fence_after();
+            float s[64];
+            tmem_ld32(tS + 64 * b, s);
+            tmem_ld32(tS + 64 * b + 32, s + 32);
+            tmem_wait_ld();
+            const int col0 = (w.unit + it) * PC_U + 64 * b;
+            if (lim_warp < col0 + 64) {
+              const int rel = lim - col0;
 #pragma unroll
-            for (int c = 0; c < 128; ++c) s[c] = c < rel ? s[c] : -INFINITY;
-          }
-          float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-          for (int c = 4; c < 128; c += 8) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mx[k] = c + 4 + k < 128 ? fmaxf(fmaxf(mx[k], s[c + k]), s[c + 4 + k]) : fmaxf(mx[k], s[c + k]);
-          }
-          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          const bool grow = mt > __fadd_rn(m, PC_GROW);  // from -inf: at the first score
-          if (__any_sync(0xffffffffu, grow)) {
-            float alpha = 1.0f;
-            if (grow) {
-              alpha = exp2_approx(__fmul_rn(__fsub_rn(m, mt), PG_SCALE_LOG2));
-              m = mt;
-              l = __fmul_rn(l, alpha);
+              for (int c = 0; c < 64; ++c) s[c] = c < rel ? s[c] : -INFINITY;
             }
-            if (it > 0) {  // this row's O: every product so far has ended, S(it) was behind them
-#pragma unroll 1
-              for (int c = 0; c < 128; c += 16) {
-                float o[16];
-                tmem_ld16f(tO + c, o);
-                tmem_wait_ld();
+            float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __fmul_rn(o[k], alpha);
-                tmem_st16(tO + c, reinterpret_cast<const uint32_t*>(o));
+            for (int c = 4; c < 60; c += 8) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], s[c + k]), s[c + 4 + k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[60 + k]);
+            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const bool grow = mt > __fadd_rn(m, PC_GROW);  // from -inf: at the first score
+            if (__any_sync(0xffffffffu, grow)) {
+              float alpha = 1.0f;
+              if (grow) {
+                alpha = exp2_approx(__fmul_rn(__fsub_rn(m, mt), PG_SCALE_LOG2));
+                m = mt;
+                l = __fmul_rn(l, alpha);
+              }
+              if (it + b > 0) {  // this row's O, once the product of the step before has ended
+                ok = warp_wait(s_full(half, b ^ 1), (ph >> (b ^ 1)) & 1u, &s_abort);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 16) {
+                  float o[16];
+                  tmem_ld16f(tO + c, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) o[k] = __fmul_rn(o[k], alpha);
+                  tmem_st16(tO + c, reinterpret_cast<const uint32_t*>(o));
+                }
               }
             }
-          }
-          const float mu = m == -INFINITY ? 0.0f : -__fmul_rn(m, PG_SCALE_LOG2);
-          const uint64_t sc2 = pack_f32x2(PG_SCALE_LOG2, PG_SCALE_LOG2), mu2 = pack_f32x2(mu, mu);
-          uint64_t sum2[2] = {0ull, 0ull};
+            const float mu = m == -INFINITY ? 0.0f : -__fmul_rn(m, PG_SCALE_LOG2);
+            const uint64_t sc2 = pack_f32x2(PG_SCALE_LOG2, PG_SCALE_LOG2), mu2 = pack_f32x2(mu, mu);
+            uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            uint32_t p[16];
+            for (int c = 0; c < 64; c += 32) {
+              uint32_t p[16];
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float x, y;
-              unpack_f32x2(fma_f32x2(pack_f32x2(s[c + k], s[c + k + 1]), sc2, mu2), x, y);
-              x = exp2_approx(x);
-              y = exp2_approx(y);
-              sum2[(k >> 1) & 1] = add_f32x2(sum2[(k >> 1) & 1], pack_f32x2(x, y));
-              p[k >> 1] = pack_bf16(x, y);
+              for (int k = 0; k < 32; k += 2) {
+                float x, y;
+                unpack_f32x2(fma_f32x2(pack_f32x2(s[c + k], s[c + k + 1]), sc2, mu2), x, y);
+                x = exp2_approx(x);
+                y = exp2_approx(y);
+                sum2[(k >> 1) & 1] = add_f32x2(sum2[(k >> 1) & 1], pack_f32x2(x, y));
+                p[k >> 1] = pack_bf16(x, y);
+              }
+              tmem_st16(tS + 64 * b + (c >> 1), p);
             }
-            tmem_st16(tS + (c >> 1), p);
-            if (c >= PC_EARLY - 32) {
-              tmem_wait_st();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0 && (c == PC_EARLY - 32 || c == 96)) mbar_arrive(p_full(half, c == 96));
-            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full(half, b));
+            float x, y;
+            unpack_f32x2(add_f32x2(sum2[0], sum2[1]), x, y);
+            l = __fadd_rn(l, __fadd_rn(x, y));
           }
-          float x, y;
-          unpack_f32x2(add_f32x2(sum2[0], sum2[1]), x, y);
-          l = __fadd_rn(l, __fadd_rn(x, y));
         }
         if (!ok) break;
-        ok = warp_wait(s_full(half), ph) && !s_abort;
-        ok = __all_sync(0xffffffffu, ok);
+        ok = warp_wait(s_full(half, 0), ph & 1u, &s_abort) && warp_wait(s_full(half, 1), (ph >> 1) & 1u, &s_abort);
         if (!ok) break;
-        ph ^= 1u;
+        ph ^= 3u;
         tc_fence_after();
         if (cnt == nu) {
           const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);  // NaN stays
@@ -341,184 +379,187 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
         }
       }
       if (threadIdx.x == 0 && w.unit > 0 && w.unit + cnt == nu)
-        a.desc[blockIdx.x] = make_int4((int)((w.pos - w.unit) / w.per), w.seq, w.head, w.tile);
+        a.desc[blockIdx.x] = w.ended();
       w.advance(a, cnt, nu);
     }
     if (!ok) s_abort = 1;
-  } else if (warp == PC_MMA_WARP) {
+  } else if (warp < PC_LOAD_WARP) {
     // ------------------------------------------------------------ products
-    int slot = 0;
-    uint32_t ph_s = 0, ph_q = 0, ph_p[2] = {0, 0};
-    bool ok = true;
-    auto next_slot = [&]() {
-      if (++slot == PC_SLOTS) {
-        slot = 0;
-        ph_s ^= 1u;
-      }
-    };
-    auto scores = [&](int h, uint32_t k_addr) {
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-        umma_bf16_ss(tmem + h * 128, umma_desc_sw128(sQ + h * PC_TILE_BYTES + off), umma_desc_sw128(k_addr + off), pc_idesc(false),
-                     kk > 0);
-      }
-    };
-    auto values = [&](int h, uint32_t v_addr, bool first, int k0, int k1) {
-#pragma unroll
-      for (int kk = k0; kk < k1; ++kk)
-        umma_bf16_ts(tmem + 256 + h * 128, tmem + h * 128 + kk * 8, pc_desc_v(v_addr + kk * 2048), pc_idesc(true),
-                     (first && kk == 0) ? 0u : 1u);
-    };
-    while (w.left > 0 && ok && !s_abort) {
-      const int nu = w.units(a), cnt = (int)min(w.left, (long long)(nu - w.unit));
-      const int nh = 2 * w.tile + 1 < ChunkTiles::blocks(a, w.n) ? 2 : 1;
-      ok = warp_wait(q_full, ph_q) && warp_wait(full(slot), ph_s);
-      if (!ok) break;
-      ph_q ^= 1u;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint32_t k = ring + slot * PC_TILE_BYTES;
-        for (int h = 0; h < nh; ++h) {
-          scores(h, k);
-          if (h == nh - 1) {
-            umma_commit(empty(slot));
-            if (cnt == 1) umma_commit(q_empty);
+    // A thread per half: one for both would spend longer issuing (each wait and commit takes it about
+    // 120 cycles) than the tensor core computing.  A half without rows passes its slots on.
+    if (elect_one()) {
+      const int h = warp - PC_MMA_WARP;
+      const uint32_t q = (sQ + h * PC_TILE_BYTES) >> 4 | PC_DESC_K;
+      int ks = 0, vs = 0;
+      uint32_t ph_k = 0, ph_v = 0, ph_q = 0, ph_p = 0, ph_f = 0;  // ph_p: per step of a unit, ph_f: per slot
+      bool ok = true;
+      while (w.left > 0 && ok && !s_abort) {
+        const int nu = w.units(a), cnt = (int)min(w.left, (long long)(nu - w.unit));
+        const bool rows = 2 * w.tile + h < ChunkTiles::blocks(a, w.n);
+        auto release = [&](uint32_t bar) {
+          if (rows) umma_commit(bar);
+          else mbar_arrive(bar);
+        };
+        auto next_k = [&]() {
+          release(k_empty(ks));
+          if (++ks == PC_KSLOTS) {
+            ks = 0;
+            ph_k ^= 1u;
           }
-          umma_commit(s_full(h));
-        }
-      }
-      __syncwarp();
-      next_slot();
-      for (int it = 0; it < cnt && ok; ++it) {
-        const int vs = slot;
-        const uint32_t v = ring + vs * PC_TILE_BYTES;
-        ok = warp_wait(full(vs), ph_s);
+        };
+        ok = mbar_wait_bounded(q_full, ph_q) && mbar_wait_bounded(k_full(ks), ph_k);
         if (!ok) break;
-        next_slot();
-        // rows behind kv in the request's last page
-        const int row0 = (w.unit + it) * PC_U, tail = w.kv - row0;
-        if (tail > 0 && tail < PC_U && (tail & (a.P - 1))) {
-          const int end = min(PC_U, (tail + a.P - 1) & ~(a.P - 1));
-          for (int i = tail * 16 + lane; i < end * 16; i += 32)
-            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(v + ((i >> 3) & 1) * 16384 + (i >> 4) * 128 + (i & 7) * 16), "r"(0)
-                         : "memory");
-          fence_proxy_async_smem();
-          __syncwarp();
+        ph_q ^= 1u;
+        tc_fence_after();
+        if (rows) {
+          const uint32_t k = (sK + ks * PC_TILE_BYTES) >> 4 | PC_DESC_K;
+          pc_scores<0>(h, q, k);
+          umma_commit(s_full(h, 0));
+          pc_scores<1>(h, q, k);
+          umma_commit(s_full(h, 1));
         }
-        for (int h = 0; h < nh; ++h) {
-          if (h == 0 && it + 1 < cnt) ok = warp_wait(full(slot), ph_s);
-          ok = ok && warp_wait(p_full(h, 0), ph_p[h]);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) values(h, v, it == 0, 0, PC_EARLY / 16);
-          __syncwarp();
-          ok = warp_wait(p_full(h, 1), ph_p[h]);
-          if (!ok) break;
-          ph_p[h] ^= 1u;
-          tc_fence_after();
-          if (elect_one()) {
-            values(h, v, false, PC_EARLY / 16, 8);
-            if (it + 1 < cnt) scores(h, ring + slot * PC_TILE_BYTES);
-            if (h == nh - 1) {
-              umma_commit(empty(vs));
-              if (it + 1 < cnt) umma_commit(empty(slot));
-              if (it + 2 == cnt) umma_commit(q_empty);
-            }
-            umma_commit(s_full(h));
+        next_k();
+        if (cnt == 1) release(q_empty);
+        for (int it = 0; it < cnt; ++it) {
+          const bool more = it + 1 < cnt;
+          ok = mbar_wait_bounded(v_full(vs), ph_v);
+          if (ok && pc_tail(a, w.kv, w.unit + it) > 0) {
+            ok = mbar_wait_bounded(v_fixed(vs), (ph_f >> vs) & 1u);
+            ph_f ^= 1u << vs;
           }
-          __syncwarp();
+          if (more) ok = ok && mbar_wait_bounded(k_full(ks), ph_k);
+          if (!ok) break;
+          if (rows) {
+            const uint32_t v = (sV + vs * PC_TILE_BYTES) >> 4 | PC_DESC_V, k = (sK + ks * PC_TILE_BYTES) >> 4 | PC_DESC_K;
+            ok = mbar_wait_bounded(p_full(h, 0), ph_p);
+            if (!ok) break;
+            tc_fence_after();
+            pc_values<0>(h, v, it == 0);
+            if (more) pc_scores<0>(h, q, k);
+            umma_commit(s_full(h, 0));
+            ok = mbar_wait_bounded(p_full(h, 1), ph_p);
+            if (!ok) break;
+            ph_p ^= 1u;
+            tc_fence_after();
+            pc_values<1>(h, v, false);
+            if (more) pc_scores<1>(h, q, k);
+          }
+          if (more) next_k();
+          if (it + 2 == cnt) release(q_empty);
+          release(v_empty(vs));
+          if (rows) umma_commit(s_full(h, 1));
+          if (++vs == PC_VSLOTS) {
+            vs = 0;
+            ph_v ^= 1u;
+          }
         }
-        if (it + 1 < cnt) next_slot();
+        w.advance(a, cnt, nu);
       }
-      w.advance(a, cnt, nu);
+      if (!ok) s_abort = 1;
+      umma_commit(mma_done);  // every product ends before tensor memory is released, also after an abort
+      mbar_drain(mma_done, 0);
     }
-    if (!ok) s_abort = 1;
-  } else if (warp == PC_KV_WARP) {
-    // ------------------------------------------------------------ K and V
+  } else {
+    // ------------------------------------------------------------ K and Q (warp 10), V (warp 11)
+    const bool is_v = warp != PC_LOAD_WARP;
+    const void* map = is_v ? &maps.v : &maps.k;
+    const uint32_t buf = is_v ? sV : sK;
+    const int slots = is_v ? PC_VSLOTS : PC_KSLOTS;
     const int log2b = min(a.log2P, 7), npg = 1 << (7 - log2b);  // rows of a copy, copies per unit and 64-column half
-    int slot = 0, issued = 0;
-    uint32_t ph = 1;
+    int slot = 0, issued = 0, q_issued = 0;
+    uint32_t ph = 1, ph_q = 1;
     bool ok = true;
     while (w.left > 0 && ok && !s_abort) {
       const int nu = w.units(a), cnt = (int)min(w.left, (long long)(nu - w.unit));
       const int vis = ChunkTiles::visible(a, w.n, w.kv, w.tile);
       const int* trow = a.table + (long long)w.seq * a.width;
-      // this lane's page of a unit: its id, or n_pages (zeros) where there is none to see
-      auto page_of = [&](int u) {
+      // this lane's entry of the table for a unit (-1 where no row sees it)
+      auto entry = [&](int u) {
         const int row = u * PC_U + (lane << log2b);
-        if (lane >= npg || row >= vis) return a.n_pages;
-        const int id = __ldg(trow + (row >> a.log2P));
-        if (id >= 0 && id < a.n_pages) return id;
-        flag_index_error();
-        return a.n_pages;
+        return lane < npg && row < vis ? __ldg(trow + (row >> a.log2P)) : -1;
       };
-      int page = page_of(w.unit);
-      for (int it = 0; it < cnt && ok; ++it) {
-        const int row = (w.unit + it) * PC_U + (lane << log2b);
-        const int cur = page;
-        if (it + 1 < cnt) page = page_of(w.unit + it + 1);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          ok = warp_wait(empty(slot), ph);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(full(slot), PC_TILE_BYTES);
+      int ahead = entry(w.unit);
+      for (int it = 0; it < cnt; ++it) {
+        const int row0 = (w.unit + it) * PC_U;
+        int page = ahead;
+        if (page < 0 || page >= a.n_pages) {  // zeros; an error where a row would see the page
+          if (lane < npg && row0 + (lane << log2b) < vis) flag_index_error();
+          page = a.n_pages;
+        }
+        if (it + 1 < cnt) ahead = entry(w.unit + it + 1);
+        const uint32_t bar_full = is_v ? v_full(slot) : k_full(slot);
+        ok = warp_wait(is_v ? v_empty(slot) : k_empty(slot), ph, &s_abort);
+        if (!ok) break;
+        if (elect_one()) mbar_arrive_expect_tx(bar_full, PC_TILE_BYTES);
+        __syncwarp();
+        const uint32_t dst = buf + slot * PC_TILE_BYTES;
+        for (int p = 0; p < npg; ++p) {
+          const int id = __shfl_sync(0xffffffffu, page, p), at = p << log2b;
+          if (elect_one()) {
+            tma_load_4d(dst + at * 128, map, 0, (row0 + at) & (a.P - 1), w.head, id, bar_full);
+            tma_load_4d(dst + at * 128 + 16384, map, 64, (row0 + at) & (a.P - 1), w.head, id, bar_full);
+          }
           __syncwarp();
-          if (lane < npg) {
-            const uint32_t dst = ring + slot * PC_TILE_BYTES + (lane << log2b) * 128;
-            const void* map = kv ? &maps.v : &maps.k;
-            tma_load_4d(dst, map, 0, row & (a.P - 1), w.head, cur, full(slot));
-            tma_load_4d(dst + 16384, map, 64, row & (a.P - 1), w.head, cur, full(slot));
+        }
+        ++issued;
+        if (is_v) {
+          // rows behind kv in the request's last page become zeros once the copy has landed
+          const int tail = pc_tail(a, w.kv, w.unit + it);
+          if (tail > 0) {
+            ok = warp_wait(bar_full, ph ^ 1u, &s_abort);
+            if (!ok) break;
+            const int end = min(PC_U, (tail + a.P - 1) & ~(a.P - 1));
+            for (int i = tail * 16 + lane; i < end * 16; i += 32)
+              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + ((i >> 3) & 1) * 16384 + (i >> 4) * 128 + (i & 7) * 16),
+                           "r"(0)
+                           : "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v_fixed(slot));
           }
-          ++issued;
-          if (++slot == PC_SLOTS) {
-            slot = 0;
-            ph ^= 1u;
+        } else if (it == 0) {
+          ok = warp_wait(q_empty, ph_q, &s_abort);
+          if (!ok) break;
+          ph_q ^= 1u;
+          if (elect_one()) {
+            const int nh = 2 * w.tile + 1 < ChunkTiles::blocks(a, w.n) ? 2 : 1;
+            mbar_arrive_expect_tx(q_full, nh * a.TB * a.GB * PG_D * 2);
+            for (int h = 0; h < nh; ++h) {
+              const ChunkRow r = chunk_row(a, w.n, w.tile, h * 128);
+              const uint32_t dst = sQ + h * PC_TILE_BYTES;
+              tma_load_4d(dst, &maps.q, 0, r.g, w.head, w.t0 + r.t, q_full);
+              tma_load_4d(dst + 16384, &maps.q, 64, r.g, w.head, w.t0 + r.t, q_full);
+            }
           }
+          __syncwarp();
+          ++q_issued;
+        }
+        if (++slot == slots) {
+          slot = 0;
+          ph ^= 1u;
         }
       }
       w.advance(a, cnt, nu);
     }
     if (!ok) s_abort = 1;
-    if (lane == 0) s_issued = issued;
-  } else if (warp == PC_Q_WARP) {
-    // ------------------------------------------------------------ Q
-    uint32_t ph = 1;
-    bool ok = true;
-    while (w.left > 0 && ok && !s_abort) {
-      const int nu = w.units(a), cnt = (int)min(w.left, (long long)(nu - w.unit));
-      ok = warp_wait(q_empty, ph);
-      if (!ok) break;
-      ph ^= 1u;
-      if (lane == 0) {
-        const int nh = 2 * w.tile + 1 < ChunkTiles::blocks(a, w.n) ? 2 : 1;
-        mbar_arrive_expect_tx(q_full, nh * a.TB * a.GB * PG_D * 2);
-        for (int h = 0; h < nh; ++h) {
-          const ChunkRow r = chunk_row(a, w.n, w.tile, h * 128);
-          const uint32_t dst = sQ + h * PC_TILE_BYTES;
-          tma_load_4d(dst, &maps.q, 0, r.g, w.head, w.t0 + r.t, q_full);
-          tma_load_4d(dst + 16384, &maps.q, 64, r.g, w.head, w.t0 + r.t, q_full);
-        }
-        ++s_q_issued;
-      }
-      __syncwarp();
-      w.advance(a, cnt, nu);
+    if (lane == 0) {
+      s_issued[is_v] = issued;
+      if (!is_v) s_q_issued = q_issued;
     }
-    if (!ok) s_abort = 1;
   }
 
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (s_abort) {
-    // every issued product ends and every issued copy lands before tensor memory is released
-    if (warp == PC_MMA_WARP && lane == 0) {
-      umma_commit(mma_done);
-      mbar_drain(mma_done, 0);
+    // every issued copy lands before the block ends
+    if (warp >= PC_LOAD_WARP && lane == 0) {
+      const bool is_v = warp != PC_LOAD_WARP;
+      const int slots = is_v ? PC_VSLOTS : PC_KSLOTS, n = s_issued[is_v];
+      for (int i = max(0, n - slots); i < n; ++i)
+        mbar_drain(is_v ? v_full(i % slots) : k_full(i % slots), (uint32_t)((i / slots) & 1));
+      if (!is_v && s_q_issued > 0) mbar_drain(q_full, (uint32_t)((s_q_issued - 1) & 1));
     }
-    if (warp == PC_Q_WARP && lane == 0 && s_q_issued > 0) mbar_drain(q_full, (uint32_t)((s_q_issued - 1) & 1));
-    if (warp == PC_KV_WARP && lane == 0)
-      for (int k = max(0, s_issued - PC_SLOTS); k < s_issued; ++k) mbar_drain(full(k % PC_SLOTS), (uint32_t)((k / PC_SLOTS) & 1));
   }
   __syncthreads();
   if (warp == PC_MMA_WARP) {
@@ -527,54 +568,19 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
   }
 }
 
-// Joins the parts of the tile that CTA c finished (blockIdx.x), as k_attn_paged_few_join does.
 // Thread: a row and 16 of its dimensions (blockIdx.y).
 __global__ void __launch_bounds__(PC_M) k_attn_paged_chunk_join(const PagedArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int c = blockIdx.x;
-  const int4 d = a.desc[c];
-  if (d.x < 0) return;
-  int t0, n, kv;
-  paged_request(a, d.y, t0, n, kv);
+  const PagedTile d = a.desc[blockIdx.x];
+  if (d.first < 0) return;
   const int row = threadIdx.x, g0 = blockIdx.y * 4;
-  const ChunkRow r = chunk_row(a, n, d.w, row);
+  const ChunkRow r = chunk_row(a, d.n, d.tile, row);
   if (!r.there) return;
-  auto part = [&](int i) { return a.part + ((long long)i * 2 + (i == d.x ? 1 : 0)) * PC_PART; };
-  float m = -INFINITY;
-  for (int i = d.x; i <= c; ++i) m = fmaxf(m, part(i)[PC_M * PG_D + row]);
-  const float mu = m == -INFINITY ? 0.0f : m;
-  float l = 0.0f, o[16];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) o[k] = 0.0f;
-  for (int i = d.x; i <= c; ++i) {
-    const float* p = part(i);
-    const float f = exp2_approx(__fmul_rn(__fsub_rn(p[PC_M * PG_D + row], mu), PG_SCALE_LOG2));
-    l = __fmaf_rn(p[PC_M * PG_D + PC_M + row], f, l);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 x = reinterpret_cast<const float4*>(p)[(g0 + k) * PC_M + row];
-      o[4 * k] = __fmaf_rn(x.x, f, o[4 * k]);
-      o[4 * k + 1] = __fmaf_rn(x.y, f, o[4 * k + 1]);
-      o[4 * k + 2] = __fmaf_rn(x.z, f, o[4 * k + 2]);
-      o[4 * k + 3] = __fmaf_rn(x.w, f, o[4 * k + 3]);
-    }
-  }
-  const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);
-  const long long off = ((long long)(t0 + r.t) * a.Hq + d.z * a.G + r.g) * PG_D + g0 * 4;
-#pragma unroll
-  for (int k = 0; k < 16; ++k) o[k] = __fmul_rn(o[k], inv);
-  if (a.out_dtype == BITNET_BF16) {
-    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + off);
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      dst[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
-                          pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
-  } else {
-    float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + off);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-  }
+  float o[16], l;
+  join_parts<4>(a.part, PC_PART, PC_M * PG_D, PC_M, row, d.first, blockIdx.x, PG_SCALE_LOG2, [&](int k) { return ((g0 + k) * PC_M + row) * 4; },
+                o, l);
+  store_row<4>(a.out, a.out_dtype, ((long long)(d.t0 + r.t) * a.Hq + d.head * a.G + r.g) * PG_D + g0 * 4, o);
 }
 
 }  // namespace bitnet

@@ -21,6 +21,11 @@
 
 namespace bitnet {
 
+// A tile whose units lie in several CTAs: `first` is the one it begins in, -1 for no tile.
+struct alignas(16) PagedTile {
+  int first, t0, n, head, tile, pad[3];
+};
+
 struct PagedArgs {
   const __nv_bfloat16* q;        // [T][Hq][128]
   const __nv_bfloat16* k_pages;  // [n_pages][Hkv][P][128]
@@ -29,9 +34,10 @@ struct PagedArgs {
   const int* cu;                 // [B + 1]
   const int* kv;                 // [B]
   void* out;                     // [T][Hq][128]
-  int4* desc;                    // [C] what a CTA's first tile is, where it ends that tile
+  PagedTile* desc;               // [C] the tile that a CTA ended and another one began
   float* part;                   // [C][2] partial tiles
   int T, B, Hq, Hkv, G, P, log2P, width, n_pages, max_new, out_dtype;
+  uint64_t by_G, by_TB, by_GB;   // ceil(2^32 / divisor), for div_small
   int TB, GB, NB;                // chunk kernel: a block of query rows is TB tokens x GB heads, NB blocks cover the G heads
 };
 
@@ -41,6 +47,14 @@ BN_DEV float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// x / d for 0 <= x < 2^22, d <= 1024, m = ceil(2^32 / d): m d - 2^32 < d, so x m / 2^32 exceeds x / d by
+// less than x d / (2^32 d) < 1 / d.
+BN_DEV int div_small(int x, uint64_t m) { return (int)(((uint64_t)(uint32_t)x * m) >> 32); }
+// a / b for non-negative numbers, most often of 32 bits (a 64-bit division takes several times as long).
+BN_DEV long long div_nonneg(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // Request i's new tokens and cache rows; false for lengths that do not fit the call.
@@ -59,7 +73,7 @@ struct FewTiles {  // 16 consecutive rows
   BN_DEV static int tiles(const PagedArgs& a, int n) { return (n * a.G + M - 1) / M; }
   BN_DEV static int visible(const PagedArgs& a, int n, int kv, int j) {
     const int last = min((j + 1) * M, n * a.G) - 1;
-    return max(0, kv - n + last / a.G + 1);
+    return max(0, kv - n + div_small(last, a.by_G) + 1);
   }
 };
 template <typename Tiles>
@@ -68,6 +82,10 @@ BN_DEV int tile_units(const PagedArgs& a, int n, int kv, int j) {
 }
 
 // A CTA's place on the line of units.
+struct PagedWalkShared {
+  long long warp_sum[32], pr0, pr1;
+  int seq, t0, n, kv, tile, unit;
+};
 template <typename Tiles>
 struct PagedWalk {
   int seq, t0, n, kv;  // request
@@ -77,78 +95,112 @@ struct PagedWalk {
   long long left;      // units of this CTA still to do
   long long per;       // units per CTA
 
-  // Units of one request and head, or 0 for a request whose lengths do not fit.
-  BN_DEV static long long request_units(const PagedArgs& a, int i, bool& bad) {
-    int t0, n, kv;
-    if (!paged_request(a, i, t0, n, kv)) {
-      bad = true;
-      return 0;
-    }
-    const int k = Tiles::tiles(a, n);
-    long long w = 0;
-    for (int j = 0; j < k; ++j) w += tile_units<Tiles>(a, n, kv, j);
-    return w;
-  }
-
-  // Block-wide: finds the CTA's share.  `sm`: 4 long longs, `red`: 32 long longs of shared memory.
-  BN_DEV void begin(const PagedArgs& a, int C, long long* sm, long long* red) {
-    bool bad = false;
+  // Block-wide: finds the CTA's share.  Up to blockDim requests are taken at once, S threads (a
+  // power of two) per request, each with q consecutive tiles of one head; prefix sums over the
+  // threads give the place of each request (times Hkv) and of each thread's tiles in a head.
+  BN_DEV void begin(const PagedArgs& a, int C, PagedWalkShared* sm) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    const long long first = threadIdx.x < a.B ? request_units(a, threadIdx.x, bad) : 0;
-    long long mine = first;
-    for (int i = threadIdx.x + blockDim.x; i < a.B; i += blockDim.x) mine += request_units(a, i, bad);
-    const long long total = block_reduce(mine, red, AddOpLL()) * a.Hkv;
-    if (bad && blockIdx.x == 0) flag_index_error();
-    if (threadIdx.x == 0) sm[0] = -1;
-    __syncthreads();
-    const long long share = (total + C - 1) / C;
-    per = share;
-    pos = (long long)blockIdx.x * share;
-    left = max(0ll, min(share, total - pos));
-    if (left == 0) return;
-    long long before = 0;
-    for (int i0 = 0; i0 < a.B; i0 += blockDim.x) {
-      const int i = i0 + threadIdx.x;
-      const long long w = (i0 == 0 ? first : (i < a.B ? request_units(a, i, bad) : 0)) * a.Hkv;
-      long long v = w;
+    int logS = 0;
+    while ((a.B << (logS + 1)) <= (int)blockDim.x) ++logS;
+    const int S = 1 << logS, sub = threadIdx.x & (S - 1), per_round = blockDim.x >> logS;
+    bool bad = false;
+    int rt0, rn, rkv, j0, j1;  // this thread's request and tiles of the last round
+    auto mine_of = [&](int i) {
+      rt0 = rn = rkv = j0 = j1 = 0;
+      if (i >= a.B) return 0ll;
+      if (!paged_request(a, i, rt0, rn, rkv)) {  // lengths that do not fit: no units
+        bad = true;
+        rn = 0;
+        return 0ll;
+      }
+      const int k = Tiles::tiles(a, rn), q = (k + S - 1) >> logS;
+      j0 = min(k, sub * q);
+      j1 = min(k, j0 + q);
+      long long w = 0;
+      for (int j = j0; j < j1; ++j) w += tile_units<Tiles>(a, rn, rkv, j);
+      return w;
+    };
+    // inclusive prefix sum over the block and its total
+    auto scan = [&](long long v, long long& all) {
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += x;
       }
-      if (lane == 31) red[warp] = v;
+      __syncthreads();  // the sums of the round before have been read
+      if (lane == 31) sm->warp_sum[warp] = v;
       __syncthreads();
-      long long base = before, all = before;
+      all = 0;
       for (int k = 0; k < nw; ++k) {
-        if (k < warp) base += red[k];
-        all += red[k];
+        const long long x = sm->warp_sum[k];
+        if (k < warp) v += x;
+        all += x;
       }
-      const long long end = base + v;
-      if (pos >= end - w && pos < end) {
-        sm[0] = i;
-        sm[1] = pos - (end - w);
-        sm[2] = w / a.Hkv;
-      }
-      __syncthreads();
-      before = all;
-      if (sm[0] >= 0) break;
+      return v;
+    };
+    if (threadIdx.x == 0) sm->seq = 0x7FFFFFFF;
+    long long total = 0, incl = 0, mine = 0, last_round = 0;
+    const int rounds = (a.B + per_round - 1) / per_round;
+    for (int r = 0; r < rounds; ++r) {
+      mine = mine_of(r * per_round + (threadIdx.x >> logS));
+      incl = total + scan(mine, last_round);
+      total += last_round;
     }
-    seq = (int)sm[0];
-    const long long off = sm[1];
-    const long long w = sm[2];
-    paged_request(a, seq, t0, n, kv);
+    if (bad && blockIdx.x == 0) flag_index_error();
+    per = div_nonneg(total * a.Hkv + C - 1, C);
+    pos = (long long)blockIdx.x * per;
+    left = max(0ll, min(per, total * a.Hkv - pos));
+    if (left == 0) return;
+    long long before = total - last_round;
+    int round = rounds - 1;
+    while (pos < before * a.Hkv) {  // from the last round, whose sums are at hand, downwards
+      --round;
+      mine = mine_of(round * per_round + (threadIdx.x >> logS));
+      long long all;
+      incl = scan(mine, all);
+      before -= all;
+      incl += before;
+    }
+    // the request: the first whose end lies behind pos (this round's are consecutive)
+    const long long start = incl - mine;
+    __syncthreads();  // the last round's sums have been read, seq is set
+    if (sub == S - 1 && pos < incl * a.Hkv) atomicMin(&sm->seq, (int)(threadIdx.x >> logS));
+    __syncthreads();
+    const bool in_request = (int)(threadIdx.x >> logS) == sm->seq;
+    if (in_request && sub == 0) {
+      sm->pr0 = start;
+      sm->t0 = rt0;
+      sm->n = rn;
+      sm->kv = rkv;
+    }
+    if (in_request && sub == S - 1) sm->pr1 = incl;
+    __syncthreads();
+    const long long w = sm->pr1 - sm->pr0, off = pos - sm->pr0 * a.Hkv;
+    head = (int)div_nonneg(off, w);
+    const long long target = sm->pr0 + (off - head * w);
+    if (in_request && target >= start && target < incl) {
+      long long rem = target - start;
+      int j = j0;
+      for (;; ++j) {
+        const int u = tile_units<Tiles>(a, rn, rkv, j);
+        if (rem < u) break;
+        rem -= u;
+      }
+      sm->tile = j;
+      sm->unit = (int)rem;
+    }
+    __syncthreads();
+    t0 = sm->t0;
+    n = sm->n;
+    kv = sm->kv;
+    tile = sm->tile;
+    unit = sm->unit;
+    seq = round * per_round + sm->seq;
     tiles = Tiles::tiles(a, n);
-    head = (int)(off / w);
-    long long rem = off - head * w;
-    tile = 0;
-    for (;;) {
-      const int u = tile_units<Tiles>(a, n, kv, tile);
-      if (rem < u) break;
-      rem -= u;
-      ++tile;
-    }
-    unit = (int)rem;
   }
+
+  // The descriptor of the tile that is ending, if it began in another CTA's share.
+  BN_DEV PagedTile ended() const { return {(int)div_nonneg(pos - unit, per), t0, n, head, tile}; }
 
   BN_DEV int units(const PagedArgs& a) const { return tile_units<Tiles>(a, n, kv, tile); }
 
@@ -226,13 +278,13 @@ BN_DEV uint32_t pack_bf16(float lo, float hi) {
 
 __global__ void __launch_bounds__(PD_THREADS, 2) k_attn_paged_few(const PagedArgs a) {
   extern __shared__ __align__(128) uint8_t pd_sm[];
-  __shared__ long long s_walk[4], s_red[32];
+  __shared__ PagedWalkShared s_walk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait();
   PagedWalk<FewTiles> w;
-  w.begin(a, gridDim.x, s_walk, s_red);
-  if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  w.begin(a, gridDim.x, &s_walk);
+  if (threadIdx.x == 0) a.desc[blockIdx.x].first = -1;
   const uint32_t ring = smem_addr(pd_sm) + warp * PD_STAGES * PD_STAGE_BYTES;
   const int g = lane >> 2, tq = lane & 3;
   const long long page_elems = (long long)a.Hkv * a.P * PG_D;
@@ -250,7 +302,7 @@ __global__ void __launch_bounds__(PD_THREADS, 2) k_attn_paged_few(const PagedArg
     for (int e = 0; e < 2; ++e) {
       const int r = r0 + g + 8 * e;
       const bool there = r < R;
-      const int t = there ? r / a.G : 0, hg = there ? r - t * a.G : 0;
+      const int t = there ? div_small(r, a.by_G) : 0, hg = there ? r - t * a.G : 0;
       lim[e] = there ? max(0, w.kv - w.n + t + 1) : 0;
       qoff[e] = there ? ((long long)(w.t0 + t) * a.Hq + w.head * a.G + hg) * PG_D : -1;
 #pragma unroll
@@ -440,54 +492,85 @@ __global__ void __launch_bounds__(PD_THREADS, 2) k_attn_paged_few(const PagedArg
           }
         }
         if (lane == 0 && w.unit > 0 && w.unit + cnt == nu)
-          a.desc[blockIdx.x] = make_int4((int)((w.pos - w.unit) / w.per), w.seq, w.head, w.tile);
+          a.desc[blockIdx.x] = w.ended();
       }
     }
     w.advance(a, cnt, nu);
   }
 }
 
-// Joins the parts of the tile that CTA c finished: part 1 of the CTA that the tile began in, and
-// part 0 of every later one up to c.  Thread: a row and eight of its dimensions.
+// Joins the parts of the tile that CTA blockIdx.x ended: part 1 of the CTA that the tile began in, and
+// part 0 of every later one.  Each thread adds up V4 float4 of one row, four parts at a time so
+// that their loads are in flight together; `at(part, k)` is the place of the row's k-th one.
+template <int V4, typename At>
+BN_DEV void join_parts(const float* parts, int stride, int stats, int rows, int row, int first, int last, float scale_log2, At at,
+                       float (&o)[4 * V4], float& l) {
+  float m = -INFINITY;
+  l = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 4 * V4; ++k) o[k] = 0.0f;
+  for (int i0 = first; i0 <= last; i0 += 4) {
+    float pm[4], pl[4];
+    float4 x[4][V4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = min(i0 + u, last);
+      const float* p = parts + ((long long)i * 2 + (i == first ? 1 : 0)) * stride;
+      pm[u] = i0 + u <= last ? p[stats + row] : -INFINITY;
+      pl[u] = p[stats + rows + row];
+#pragma unroll
+      for (int k = 0; k < V4; ++k) x[u][k] = *reinterpret_cast<const float4*>(p + at(k));
+    }
+    const float mn = fmaxf(fmaxf(m, fmaxf(pm[0], pm[1])), fmaxf(pm[2], pm[3]));
+    const float mu = mn == -INFINITY ? 0.0f : mn;
+    const float old = exp2_approx(__fmul_rn(__fsub_rn(m, mu), scale_log2));
+    m = mn;
+    l = __fmul_rn(l, old);
+#pragma unroll
+    for (int k = 0; k < 4 * V4; ++k) o[k] = __fmul_rn(o[k], old);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float f = exp2_approx(__fmul_rn(__fsub_rn(pm[u], mu), scale_log2));  // 0 behind the last part
+      l = __fmaf_rn(pl[u], f, l);
+#pragma unroll
+      for (int k = 0; k < V4; ++k) {
+        o[4 * k] = __fmaf_rn(x[u][k].x, f, o[4 * k]);
+        o[4 * k + 1] = __fmaf_rn(x[u][k].y, f, o[4 * k + 1]);
+        o[4 * k + 2] = __fmaf_rn(x[u][k].z, f, o[4 * k + 2]);
+        o[4 * k + 3] = __fmaf_rn(x[u][k].w, f, o[4 * k + 3]);
+      }
+    }
+  }
+  const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);  // NaN stays
+#pragma unroll
+  for (int k = 0; k < 4 * V4; ++k) o[k] = __fmul_rn(o[k], inv);
+}
+template <int V4>
+BN_DEV void store_row(void* out, int out_dtype, long long off, const float (&o)[4 * V4]) {
+  if (out_dtype == BITNET_BF16) {
+    uint2* dst = reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out) + off);
+#pragma unroll
+    for (int k = 0; k < V4; ++k) dst[k] = make_uint2(pack_bf16(o[4 * k], o[4 * k + 1]), pack_bf16(o[4 * k + 2], o[4 * k + 3]));
+  } else {
+    float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + off);
+#pragma unroll
+    for (int k = 0; k < V4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+  }
+}
+
+// Thread: a row and eight of its dimensions.
 __global__ void __launch_bounds__(256) k_attn_paged_few_join(const PagedArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int c = blockIdx.x;
-  const int4 d = a.desc[c];
-  if (d.x < 0) return;
-  int t0, n, kv;
-  paged_request(a, d.y, t0, n, kv);
+  const PagedTile d = a.desc[blockIdx.x];
+  if (d.first < 0) return;
   const int row = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * 8;
-  const int r = d.w * PD_M + row;
-  if (r >= n * a.G) return;
-  auto part = [&](int i) { return a.part + ((long long)i * 2 + (i == d.x ? 1 : 0)) * PD_PART; };
-  float m = -INFINITY;
-  for (int i = d.x; i <= c; ++i) m = fmaxf(m, part(i)[PD_M * PG_D + row]);
-  const float mu = m == -INFINITY ? 0.0f : m;
-  float l = 0.0f, o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  for (int i = d.x; i <= c; ++i) {
-    const float* p = part(i);
-    const float f = exp2_approx(__fsub_rn(p[PD_M * PG_D + row], mu));
-    l = __fmaf_rn(p[PD_M * PG_D + PD_M + row], f, l);
-    const float4 x = *reinterpret_cast<const float4*>(p + row * PG_D + d0);
-    const float4 y = *reinterpret_cast<const float4*>(p + row * PG_D + d0 + 4);
-    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] = __fmaf_rn(v[k], f, o[k]);
-  }
-  const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);
-  const int t = r / a.G;
-  const long long off = ((long long)(t0 + t) * a.Hq + d.z * a.G + (r - t * a.G)) * PG_D + d0;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) o[k] = __fmul_rn(o[k], inv);
-  if (a.out_dtype == BITNET_BF16) {
-    *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + off) =
-        make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
-  } else {
-    float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + off);
-    dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_float4(o[4], o[5], o[6], o[7]);
-  }
+  const int r = d.tile * PD_M + row;
+  if (r >= d.n * a.G) return;
+  float o[8], l;
+  join_parts<2>(a.part, PD_PART, PD_M * PG_D, PD_M, row, d.first, blockIdx.x, 1.0f, [&](int k) { return row * PG_D + d0 + 4 * k; }, o, l);
+  const int t = div_small(r, a.by_G);
+  store_row<2>(a.out, a.out_dtype, ((long long)(d.t0 + t) * a.Hq + d.head * a.G + (r - t * a.G)) * PG_D + d0, o);
 }
 
 }  // namespace bitnet

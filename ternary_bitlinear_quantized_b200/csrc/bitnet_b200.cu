@@ -1331,13 +1331,13 @@ constexpr int64_t PAGED_FEW_ROWS = 64;
 static bool paged_few(int64_t G, int64_t max_new) { return max_new * G <= PAGED_FEW_ROWS; }
 static int paged_ctas(bool few) { return (few ? 2 : 1) * device_sm_count(); }
 
-// The workspace: tile descriptors (16 bytes per CTA) and two partial tiles per CTA.
+// The workspace: a tile descriptor and two partial tiles per CTA.
 
 size_t bitnet_attention_paged_workspace_bytes(int64_t Hq, int64_t Hkv, int64_t max_new) {
   if (Hq <= 0 || Hkv <= 0 || Hq > 1024 || Hq % Hkv || max_new < 0) return 0;
   const bool few = paged_few(Hq / Hkv, max_new);
   const size_t ctas = (size_t)paged_ctas(few);
-  return align_up(ctas * 16) + align_up(ctas * 2 * (few ? PD_PART : PC_PART) * 4);
+  return align_up(ctas * sizeof(PagedTile)) + align_up(ctas * 2 * (few ? PD_PART : PC_PART) * 4);
 }
 
 bitnet_status bitnet_attention_paged(const void* q_rot, const void* k_pages, const void* v_pages,
@@ -1380,12 +1380,16 @@ bitnet_status bitnet_attention_paged(const void* q_rot, const void* k_pages, con
   a.GB = a.G < 128 ? a.G : 128;
   a.TB = 128 / a.GB;
   a.NB = (a.G + 127) / 128;
+  auto by = [](int d) { return (uint64_t)(((1ull << 32) + d - 1) / d); };
+  a.by_G = by(a.G);
+  a.by_TB = by(a.TB);
+  a.by_GB = by(a.GB);
   a.out_dtype = ot;
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
   const bool few = paged_few(a.G, max_new);
   const int ctas = paged_ctas(few);
-  a.desc = reinterpret_cast<int4*>(w);
-  a.part = reinterpret_cast<float*>(w + align_up((size_t)ctas * 16));
+  a.desc = reinterpret_cast<PagedTile*>(w);
+  a.part = reinterpret_cast<float*>(w + align_up((size_t)ctas * sizeof(PagedTile)));
   cudaError_t e;
   if (few) {
     e = opt_in_smem((const void*)k_attn_paged_few, 14);
