@@ -5,8 +5,8 @@
 //                   tensor memory, maximum, weights (bf16) back to tensor memory; the output at the end
 //   warps 8, 9      one thread each, for the rows 0-127 and 128-255: tcgen05.mma S = Q K^T (both
 //                   operands in shared memory) and O += P V (P in tensor memory)
-//   warp 10         TMA loads of K, page by page, into a ring of three 32 KB slots, and of Q
-//   warp 11         TMA loads of V into a ring of two
+//   warp 10         TMA loads of K, page by page, into a ring of two 32 KB slots, and of Q
+//   warp 11         TMA loads of V into another
 // The two halves take turns: while one half's softmax runs, the tensor core does the other's
 // products.  Tensor memory (512 columns): S of each half 128 columns, of which P takes the first 64
 // once the scores are in registers; O of each half 128 columns.
@@ -32,9 +32,9 @@ namespace bitnet {
 // one box of q holds it: GB = min(G, 128), TB = 128 / GB; NB = ceil(G / 128) blocks cover a token's
 // heads.  A tile is two consecutive blocks of a request and key/value head.
 struct ChunkTiles {
-  static constexpr int M = 256, U = 128;
+  static constexpr int M = 256, U = 128, FIXED = 2;
   BN_DEV static int blocks(const PagedArgs& a, int n) { return div_small(n + a.TB - 1, a.by_TB) * a.NB; }
-  BN_DEV static int tiles(const PagedArgs& a, int n) { return (blocks(a, n) + 1) >> 1; }
+  BN_DEV static int tiles(int blocks) { return (blocks + 1) >> 1; }
   BN_DEV static int visible(const PagedArgs& a, int n, int kv, int j) {
     const int b = 2 * j + 1, group = a.NB == 1 ? b : b / a.NB;
     return max(0, kv - n + min(n, (group + 1) * a.TB));
@@ -58,9 +58,9 @@ constexpr int PC_M = ChunkTiles::M;
 constexpr int PC_U = ChunkTiles::U;
 constexpr int PC_THREADS = 384;
 constexpr int PC_MMA_WARP = 8, PC_LOAD_WARP = 10;  // two warps each
-constexpr int PC_KSLOTS = 3, PC_VSLOTS = 2;
+constexpr int PC_KSLOTS = 2, PC_VSLOTS = 2;
 constexpr uint32_t PC_TILE_BYTES = 128 * 256;  // 128 rows of 128 bf16: two 64-column halves of 128-byte rows, swizzled
-constexpr int PC_SMEM = (2 + PC_KSLOTS + PC_VSLOTS) * PC_TILE_BYTES + 1024;
+constexpr int PC_SMEM = (3 + PC_KSLOTS + PC_VSLOTS) * PC_TILE_BYTES + 1024;  // Q, K, V, 4 KB per softmax warp
 constexpr int PC_PART = PC_M * (PG_D + 2);     // floats of a partial tile: values [32][256 rows][4], maxima, sums
 constexpr float PC_GROW = 8.0f / PG_SCALE_LOG2;
 
@@ -128,6 +128,9 @@ BN_DEV void tmem_st16(uint32_t taddr, const uint32_t* v) {
       ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
         "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+BN_DEV void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 BN_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -239,13 +242,6 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
   w.begin(a, gridDim.x, &s_walk);
   if (threadIdx.x == 0) a.desc[blockIdx.x].first = -1;
 
-  // The launch gives every thread at most 168 registers (65536 / 384); the softmax warps, which hold a
-  // row of scores, take 208: 8 * 32 * 208 + 4 * 32 * 80 <= 384 * 168 holds for the whole block.
-  if (warp < 8)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-  else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-
   if (warp < 8) {
     // ------------------------------------------------------------ softmax, one row per thread
     const int half = warp >> 2, row = half * 128 + (warp & 3) * 32 + lane;
@@ -253,15 +249,15 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
     const uint32_t tS = tmem + t_lane + half * 128, tO = tmem + t_lane + 256 + half * 128;
     uint32_t ph = 0;  // parities of s_full, a bit per step
     bool ok = true;
-    while (w.left > 0 && ok) {
-      const int nu = w.units(a), cnt = (int)min(w.left, (long long)(nu - w.unit));
-      if (2 * w.tile + half < ChunkTiles::blocks(a, w.n)) {
+    while (ok && w.take(a)) {
+      const int cnt = w.cnt;
+      if (2 * w.tile + half < w.blocks) {
         const ChunkRow r = chunk_row(a, w.n, w.tile, row);
         const int lim = r.there ? max(0, w.kv - w.n + r.t + 1) : 0x7FFFFFFF;  // rows of the cache that this row sees
         const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
         float m = -INFINITY, l = 0.0f;  // running maximum of the raw scores (may trail by 2^8), sum
         for (int it = 0; it < cnt && ok; ++it) {
-#pragma unroll
+#pragma unroll 1  // one copy of the code: the loops of all roles have to fit the instruction cache
           for (int b = 0; b < 2; ++b) {
             ok = warp_wait(s_full(half, b), (ph >> b) & 1u, &s_abort);
             if (!ok) break;
@@ -340,28 +336,41 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
         if (!ok) break;
         ph ^= 3u;
         tc_fence_after();
-        if (cnt == nu) {
+        if (cnt == w.nu) {
+          // By way of shared memory, so that a warp writes whole 128-byte lines: 32 rows of 128 bytes
+          // (64 bf16 or 32 fp32 columns), their 16-byte chunks permuted by the row.
           const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);  // NaN stays
-          const long long off = ((long long)(w.t0 + r.t) * a.Hq + w.head * a.G + r.g) * PG_D;
+          const bool bf = a.out_dtype == BITNET_BF16;
+          const long long off = r.there ? ((long long)(w.t0 + r.t) * a.Hq + w.head * a.G + r.g) * (bf ? PG_D * 2 : PG_D * 4) : -1;
+          const uint32_t stage = sV + PC_VSLOTS * PC_TILE_BYTES + warp * 4096;
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
+          for (int g = 0; g < 4; ++g) {
             float o[32];
-            tmem_ld32(tO + c, o);
+            tmem_ld32(tO + 32 * g, o);
             tmem_wait_ld();
-            if (!r.there) continue;
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = l == 0.0f ? 0.0f : __fmul_rn(o[k], inv);
-            if (a.out_dtype == BITNET_BF16) {
-              uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + off + c);
+            if (bf) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                dst[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
-                                    pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
+                sts128(stage + lane * 128 + ((((g & 1) * 4 + k) ^ (lane & 7)) << 4), pack_bf16(o[8 * k], o[8 * k + 1]),
+                       pack_bf16(o[8 * k + 2], o[8 * k + 3]), pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
+              if ((g & 1) == 0) continue;
             } else {
-              float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + off + c);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              for (int k = 0; k < 8; ++k)
+                sts128(stage + lane * 128 + ((k ^ (lane & 7)) << 4), __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
+                       __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
             }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int rr = i * 4 + (lane >> 3), ch = lane & 7;
+              const uint4 x = lds128(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
+              const long long to = __shfl_sync(0xffffffffu, off, rr);
+              if (to >= 0) *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.out) + to + (bf ? (g >> 1) : g) * 128 + ch * 16) = x;
+            }
+            __syncwarp();
           }
         } else {
           float* part = a.part + ((long long)blockIdx.x * 2 + (w.unit > 0 ? 0 : 1)) * PC_PART;
@@ -378,9 +387,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
           part[PC_M * PG_D + PC_M + row] = l;
         }
       }
-      if (threadIdx.x == 0 && w.unit > 0 && w.unit + cnt == nu)
+      if (threadIdx.x == 0 && w.unit > 0 && w.unit + cnt == w.nu)
         a.desc[blockIdx.x] = w.ended();
-      w.advance(a, cnt, nu);
     }
     if (!ok) s_abort = 1;
   } else if (warp < PC_LOAD_WARP) {
@@ -393,9 +401,9 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
       int ks = 0, vs = 0;
       uint32_t ph_k = 0, ph_v = 0, ph_q = 0, ph_p = 0, ph_f = 0;  // ph_p: per step of a unit, ph_f: per slot
       bool ok = true;
-      while (w.left > 0 && ok && !s_abort) {
-        const int nu = w.units(a), cnt = (int)min(w.left, (long long)(nu - w.unit));
-        const bool rows = 2 * w.tile + h < ChunkTiles::blocks(a, w.n);
+      while (ok && !s_abort && w.take(a)) {
+        const int cnt = w.cnt;
+        const bool rows = 2 * w.tile + h < w.blocks;
         auto release = [&](uint32_t bar) {
           if (rows) umma_commit(bar);
           else mbar_arrive(bar);
@@ -453,8 +461,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
             ph_v ^= 1u;
           }
         }
-        w.advance(a, cnt, nu);
-      }
+        }
       if (!ok) s_abort = 1;
       umma_commit(mma_done);  // every product ends before tensor memory is released, also after an abort
       mbar_drain(mma_done, 0);
@@ -469,8 +476,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
     int slot = 0, issued = 0, q_issued = 0;
     uint32_t ph = 1, ph_q = 1;
     bool ok = true;
-    while (w.left > 0 && ok && !s_abort) {
-      const int nu = w.units(a), cnt = (int)min(w.left, (long long)(nu - w.unit));
+    while (ok && !s_abort && w.take(a)) {
+      const int cnt = w.cnt;
       const int vis = ChunkTiles::visible(a, w.n, w.kv, w.tile);
       const int* trow = a.table + (long long)w.seq * a.width;
       // this lane's entry of the table for a unit (-1 where no row sees it)
@@ -490,17 +497,21 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
         const uint32_t bar_full = is_v ? v_full(slot) : k_full(slot);
         ok = warp_wait(is_v ? v_empty(slot) : k_empty(slot), ph, &s_abort);
         if (!ok) break;
-        if (elect_one()) mbar_arrive_expect_tx(bar_full, PC_TILE_BYTES);
-        __syncwarp();
         const uint32_t dst = buf + slot * PC_TILE_BYTES;
-        for (int p = 0; p < npg; ++p) {
-          const int id = __shfl_sync(0xffffffffu, page, p), at = p << log2b;
-          if (elect_one()) {
-            tma_load_4d(dst + at * 128, map, 0, (row0 + at) & (a.P - 1), w.head, id, bar_full);
-            tma_load_4d(dst + at * 128 + 16384, map, 64, (row0 + at) & (a.P - 1), w.head, id, bar_full);
-          }
-          __syncwarp();
+        int id[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p) id[p] = __shfl_sync(0xffffffffu, page, p);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar_full, PC_TILE_BYTES);
+#pragma unroll
+          for (int p = 0; p < 8; ++p)
+            if (p < npg) {
+              const int at = p << log2b;
+              tma_load_4d(dst + at * 128, map, 0, (row0 + at) & (a.P - 1), w.head, id[p], bar_full);
+              tma_load_4d(dst + at * 128 + 16384, map, 64, (row0 + at) & (a.P - 1), w.head, id[p], bar_full);
+            }
         }
+        __syncwarp();
         ++issued;
         if (is_v) {
           // rows behind kv in the request's last page become zeros once the copy has landed
@@ -510,9 +521,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
             if (!ok) break;
             const int end = min(PC_U, (tail + a.P - 1) & ~(a.P - 1));
             for (int i = tail * 16 + lane; i < end * 16; i += 32)
-              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + ((i >> 3) & 1) * 16384 + (i >> 4) * 128 + (i & 7) * 16),
-                           "r"(0)
-                           : "memory");
+              sts128(dst + ((i >> 3) & 1) * 16384 + (i >> 4) * 128 + (i & 7) * 16, 0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(v_fixed(slot));
@@ -522,7 +531,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
           if (!ok) break;
           ph_q ^= 1u;
           if (elect_one()) {
-            const int nh = 2 * w.tile + 1 < ChunkTiles::blocks(a, w.n) ? 2 : 1;
+            const int nh = 2 * w.tile + 1 < w.blocks ? 2 : 1;
             mbar_arrive_expect_tx(q_full, nh * a.TB * a.GB * PG_D * 2);
             for (int h = 0; h < nh; ++h) {
               const ChunkRow r = chunk_row(a, w.n, w.tile, h * 128);
@@ -539,7 +548,6 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
           ph ^= 1u;
         }
       }
-      w.advance(a, cnt, nu);
     }
     if (!ok) s_abort = 1;
     if (lane == 0) {

@@ -66,11 +66,13 @@ BN_DEV bool paged_request(const PagedArgs& a, int i, int& t0, int& n, int& kv) {
   return t0 >= 0 && t1 >= t0 && t1 <= a.T && n <= a.max_new && kv >= 0 && kv <= (long long)a.width * a.P;
 }
 
-// How a kernel cuts a request's query rows (of one key/value head) into tiles, and how many cache
-// rows the last row of tile j sees (0 where it sees none).
+// How a kernel cuts a request's query rows (of one key/value head) into blocks and those into tiles,
+// and how many cache rows the last row of tile j sees (0 where it sees none).  FIXED: what a tile
+// costs beside its units, in units.
 struct FewTiles {  // 16 consecutive rows
-  static constexpr int M = 16, U = 64;
-  BN_DEV static int tiles(const PagedArgs& a, int n) { return (n * a.G + M - 1) / M; }
+  static constexpr int M = 16, U = 64, FIXED = 1;
+  BN_DEV static int blocks(const PagedArgs& a, int n) { return (n * a.G + M - 1) / M; }
+  BN_DEV static int tiles(int blocks) { return blocks; }
   BN_DEV static int visible(const PagedArgs& a, int n, int kv, int j) {
     const int last = min((j + 1) * M, n * a.G) - 1;
     return max(0, kv - n + div_small(last, a.by_G) + 1);
@@ -84,16 +86,48 @@ BN_DEV int tile_units(const PagedArgs& a, int n, int kv, int j) {
 // A CTA's place on the line of units.
 struct PagedWalkShared {
   long long warp_sum[32], pr0, pr1;
-  int seq, t0, n, kv, tile, unit;
+  int seq, t0, n, kv, tile, at;
 };
 template <typename Tiles>
 struct PagedWalk {
   int seq, t0, n, kv;  // request
-  int head, tile, tiles;
-  int unit;            // next unit of the tile
-  long long pos;       // its place on the line
-  long long left;      // units of this CTA still to do
-  long long per;       // units per CTA
+  int head, tile, blocks;
+  int unit, cnt, nu;   // this piece of the tile: cnt of its nu units, from `unit` on
+  int at;              // its place in the tile, the FIXED cost included
+  int took;            // its length there
+  long long pos, left; // the place of the piece on the line, and what is left of the CTA's share from there on
+  long long per;       // the share of every CTA
+
+  // Goes on to the next piece of the CTA's share; false at its end.  A piece that lies within its
+  // tile's fixed cost has no units and is passed over.
+  BN_DEV bool take(const PagedArgs& a) {
+    for (;;) {
+      left -= took;
+      if (left <= 0) return false;
+      pos += took;
+      at += took;
+      if (at >= nu + Tiles::FIXED) {
+        at = 0;
+        if (++tile >= Tiles::tiles(blocks)) {
+          tile = 0;
+          if (++head >= a.Hkv) {
+            head = 0;
+            do {  // something is left, so a request with tokens follows
+              ++seq;
+            } while (!paged_request(a, seq, t0, n, kv) || n == 0);
+            blocks = Tiles::blocks(a, n);
+          }
+        }
+        nu = tile_units<Tiles>(a, n, kv, tile);
+      }
+      took = (int)min(left, (long long)(nu + Tiles::FIXED - at));
+      unit = max(0, at - Tiles::FIXED);
+      cnt = at + took - Tiles::FIXED - unit;
+      if (cnt > 0) return true;
+    }
+  }
+  // The descriptor of this tile, which began in another CTA's share.
+  BN_DEV PagedTile ended() const { return {(int)div_nonneg(pos - at + Tiles::FIXED, per), t0, n, head, tile}; }
 
   // Block-wide: finds the CTA's share.  Up to blockDim requests are taken at once, S threads (a
   // power of two) per request, each with q consecutive tiles of one head; prefix sums over the
@@ -113,11 +147,11 @@ struct PagedWalk {
         rn = 0;
         return 0ll;
       }
-      const int k = Tiles::tiles(a, rn), q = (k + S - 1) >> logS;
+      const int k = Tiles::tiles(Tiles::blocks(a, rn)), q = (k + S - 1) >> logS;
       j0 = min(k, sub * q);
       j1 = min(k, j0 + q);
       long long w = 0;
-      for (int j = j0; j < j1; ++j) w += tile_units<Tiles>(a, rn, rkv, j);
+      for (int j = j0; j < j1; ++j) w += tile_units<Tiles>(a, rn, rkv, j) + Tiles::FIXED;
       return w;
     };
     // inclusive prefix sum over the block and its total
@@ -150,6 +184,7 @@ struct PagedWalk {
     per = div_nonneg(total * a.Hkv + C - 1, C);
     pos = (long long)blockIdx.x * per;
     left = max(0ll, min(per, total * a.Hkv - pos));
+    took = 0;
     if (left == 0) return;
     long long before = total - last_round;
     int round = rounds - 1;
@@ -182,43 +217,22 @@ struct PagedWalk {
       long long rem = target - start;
       int j = j0;
       for (;; ++j) {
-        const int u = tile_units<Tiles>(a, rn, rkv, j);
+        const int u = tile_units<Tiles>(a, rn, rkv, j) + Tiles::FIXED;
         if (rem < u) break;
         rem -= u;
       }
       sm->tile = j;
-      sm->unit = (int)rem;
+      sm->at = (int)rem;
     }
     __syncthreads();
     t0 = sm->t0;
     n = sm->n;
     kv = sm->kv;
     tile = sm->tile;
-    unit = sm->unit;
+    at = sm->at;
     seq = round * per_round + sm->seq;
-    tiles = Tiles::tiles(a, n);
-  }
-
-  // The descriptor of the tile that is ending, if it began in another CTA's share.
-  BN_DEV PagedTile ended() const { return {(int)div_nonneg(pos - unit, per), t0, n, head, tile}; }
-
-  BN_DEV int units(const PagedArgs& a) const { return tile_units<Tiles>(a, n, kv, tile); }
-
-  // Goes on behind `cnt` units of the tile.
-  BN_DEV void advance(const PagedArgs& a, int cnt, int tile_total) {
-    left -= cnt;
-    pos += cnt;
-    unit += cnt;
-    if (left == 0 || unit < tile_total) return;
-    unit = 0;
-    if (++tile < tiles) return;
-    tile = 0;
-    if (++head < a.Hkv) return;
-    head = 0;
-    do {  // units are left, so a request with tokens follows
-      ++seq;
-    } while (!paged_request(a, seq, t0, n, kv) || n == 0);
-    tiles = Tiles::tiles(a, n);
+    blocks = Tiles::blocks(a, n);
+    nu = tile_units<Tiles>(a, n, kv, tile);
   }
 };
 
@@ -289,9 +303,8 @@ __global__ void __launch_bounds__(PD_THREADS, 2) k_attn_paged_few(const PagedArg
   const int g = lane >> 2, tq = lane & 3;
   const long long page_elems = (long long)a.Hkv * a.P * PG_D;
 
-  while (w.left > 0) {
-    const int nu = w.units(a);
-    const int cnt = (int)min(w.left, (long long)(nu - w.unit));
+  while (w.take(a)) {
+    const int nu = w.nu, cnt = w.cnt;
     const int R = w.n * a.G, r0 = w.tile * PD_M;
     const int vis = FewTiles::visible(a, w.n, w.kv, w.tile);
     // this thread's two query rows (g and g + 8 of the tile): what they see, and their q fragments
@@ -495,7 +508,6 @@ __global__ void __launch_bounds__(PD_THREADS, 2) k_attn_paged_few(const PagedArg
           a.desc[blockIdx.x] = w.ended();
       }
     }
-    w.advance(a, cnt, nu);
   }
 }
 
