@@ -124,8 +124,9 @@ def _ptr(t: torch.Tensor | None):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())  # torch.cuda.current_stream() takes 3 us
 
 
 def _dtype_code(dt: torch.dtype) -> int:
@@ -409,19 +410,41 @@ def attention_decode(q_rot, k_cache, v_cache, pos0: int, out_dtype=torch.bfloat1
 
 # ------------------------------------------------------- a serving step over a paged KV cache
 
-_I32, _F32T, _BF16T = torch.int32, torch.float32, torch.bfloat16
+# These calls are made once per layer and step, often with a few tokens: their checks are written for
+# a host time of a few microseconds.
+
+_I32, _F32T, _BF16T, _I8 = torch.int32, torch.float32, torch.bfloat16, torch.int8
+
+try:  # the allocation of torch's own generated code: half the time of torch.empty
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:
+    def _empty_strided_cuda(size, stride, dtype):
+        return torch.empty(size, dtype=dtype, device="cuda")
 
 
-def _same_device(dev: torch.device, name: str, t: torch.Tensor, dtypes: tuple) -> None:
-    if not t.is_cuda or t.device != dev or not t.is_contiguous() or t.dtype not in dtypes:
-        raise ValueError(f"{name} must be a contiguous tensor on {dev} of type {' or '.join(map(str, dtypes))}")
-
-
-def _current(t: torch.Tensor, name: str) -> torch.device:
+def _current(t: torch.Tensor, name: str) -> int:
     """The device of a call's first tensor, which has to be the current one (the stream is its)."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
-    return t.device
+    return dev
+
+
+def _arg(dev: int, name: str, t: torch.Tensor, dtype, numel: int) -> int:
+    """A contiguous tensor's address."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on cuda:{dev} of type {dtype}")
+    if t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} entries")
+    return t.data_ptr()
+
+
+def _float_code(name: str, t: torch.Tensor) -> int:
+    if t.dtype is _BF16T:
+        return BF16
+    if t.dtype is _F32T:
+        return F32
+    raise ValueError(f"{name} must be of type {_BF16T} or {_F32T}")
 
 
 def add_rmsnorm_quant_act(x, residual, gain, eps: float = 1e-6, residual_out=None, out=None, stream=None):
@@ -430,32 +453,27 @@ def add_rmsnorm_quant_act(x, residual, gain, eps: float = 1e-6, residual_out=Non
     ``residual`` itself."""
     dev = _current(x, "x")
     T, K = x.shape
-    _same_device(dev, "x", x, (_BF16T, _F32T))
-    _same_device(dev, "residual", residual, (_BF16T, _F32T))
+    n, xt, rt = T * K, _float_code("x", x), _float_code("residual", residual)
     if residual.shape != x.shape:
         raise ValueError("residual must have the shape of x")
-    if gain is not None:
-        _same_device(dev, "gain", gain, (_F32T,))
-        if gain.numel() != K:
-            raise ValueError("gain must have K entries")
     if residual_out is None:
-        residual_out = torch.empty_like(residual)
+        residual_out = _empty_strided_cuda((T, K), (K, 1), residual.dtype)
+        to = residual_out.data_ptr()
     else:
-        _same_device(dev, "residual_out", residual_out, (residual.dtype,))
         if residual_out.shape != x.shape:
             raise ValueError("residual_out must have the shape of x")
+        to = _arg(dev, "residual_out", residual_out, residual.dtype, n)
     if out is None:
-        out = (torch.empty(T, K, dtype=torch.int8, device=dev), torch.empty(T, dtype=_F32T, device=dev),
-               torch.empty(T, dtype=_I32, device=dev))
+        q, s, sq = _empty_strided_cuda((T, K), (K, 1), _I8), _empty_strided_cuda((T,), (1,), _F32T), _empty_strided_cuda((T,), (1,), _I32)
+        pq, ps, psq = q.data_ptr(), s.data_ptr(), sq.data_ptr()
     else:
-        for t, n, dt, nm in zip(out, (T * K, T, T), (torch.int8, _F32T, _I32), ("q", "s_x", "sum_q")):
-            _same_device(dev, nm, t, (dt,))
-            if t.numel() != n:
-                raise ValueError(f"{nm} must have {n} entries")
-    q, s, sq = out
-    _check(lib().bitnet_add_rmsnorm_quant_act(_ptr(x), _dtype_code(x.dtype), _ptr(residual), _dtype_code(residual.dtype),
-                                              _ptr(gain), eps, T, K, _ptr(residual_out), _ptr(q), _ptr(s), _ptr(sq),
-                                              _stream(stream)), "add_rmsnorm_quant_act")
+        q, s, sq = out
+        pq, ps, psq = _arg(dev, "q", q, _I8, n), _arg(dev, "s_x", s, _F32T, T), _arg(dev, "sum_q", sq, _I32, T)
+    st = lib().bitnet_add_rmsnorm_quant_act(
+        _arg(dev, "x", x, x.dtype, n), xt, _arg(dev, "residual", residual, residual.dtype, n), rt,
+        None if gain is None else _arg(dev, "gain", gain, _F32T, K), eps, T, K, to, pq, ps, psq, _stream(stream))
+    if st:
+        raise BitnetError(st, "add_rmsnorm_quant_act")
     return residual_out, q, s, sq
 
 
@@ -464,37 +482,36 @@ def paged_plan(new_lens, ctx_lens, block_table, free_pages, n_free, page_size: i
     n_free_out [1]); the requests' new pages are written into ``block_table`` [B, width].  All int32."""
     dev = _current(new_lens, "new_lens")
     B, width = block_table.shape
-    for t, n, nm in ((new_lens, B, "new_lens"), (ctx_lens, B, "ctx_lens"), (block_table, B * width, "block_table"),
-                     (free_pages, free_pages.numel(), "free_pages"), (n_free, 1, "n_free")):
-        _same_device(dev, nm, t, (_I32,))
-        if t.numel() != n:
-            raise ValueError(f"{nm} must have {n} entries")
-    sizes = (B + 1, B, T, T, 1)
     if T < 0:
         raise BitnetError(2, "paged_plan")
+    n_list, free_now = free_pages.numel(), _arg(dev, "n_free", n_free, _I32, 1)
     if out is None:
         # one allocation; every part starts on a 4-byte boundary, which is all the step's calls need
-        out = torch.empty(2 * B + 2 + 2 * T, dtype=_I32, device=dev).split_with_sizes(sizes)
+        buf = _empty_strided_cuda((2 * B + 2 + 2 * T,), (1,), _I32)
+        out = buf.split_with_sizes((B + 1, B, T, T, 1))
+        p = buf.data_ptr()
+        to = (p, p + 4 * (B + 1), p + 4 * (2 * B + 1), p + 4 * (2 * B + 1 + T), p + 4 * (2 * B + 1 + 2 * T))
     else:
-        for t, n, nm in zip(out, sizes, ("cu_new", "kv_lens", "positions", "slots", "n_free_out")):
-            _same_device(dev, nm, t, (_I32,))
-            if t.numel() != n:
-                raise ValueError(f"{nm} must have {n} entries")
+        to = [_arg(dev, nm, t, _I32, n) for nm, t, n in
+              zip(("cu_new", "kv_lens", "positions", "slots", "n_free_out"), out, (B + 1, B, T, T, 1), strict=True)]
+        if free_now == to[4]:
+            raise ValueError("n_free_out must not be n_free")
     cu, kv, pos, slots, left = out
-    if left.data_ptr() == n_free.data_ptr():
-        raise ValueError("n_free_out must not be n_free")
-    _check(lib().bitnet_paged_plan(_ptr(new_lens), _ptr(ctx_lens), B, page_size, _ptr(block_table), width,
-                                   _ptr(free_pages), free_pages.numel(), _ptr(n_free), T, _ptr(cu), _ptr(kv), _ptr(pos),
-                                   _ptr(slots), _ptr(left), _stream(stream)), "paged_plan")
+    st = lib().bitnet_paged_plan(
+        _arg(dev, "new_lens", new_lens, _I32, B), _arg(dev, "ctx_lens", ctx_lens, _I32, B), B, page_size,
+        _arg(dev, "block_table", block_table, _I32, B * width), width, _arg(dev, "free_pages", free_pages, _I32, n_list), n_list,
+        free_now, T, *to, _stream(stream))
+    if st:
+        raise BitnetError(st, "paged_plan")
     return cu, kv, pos, slots, left
 
 
-def _pages(dev, k_pages, v_pages, Hkv: int, d: int):
-    _same_device(dev, "k_pages", k_pages, (_BF16T,))
-    _same_device(dev, "v_pages", v_pages, (_BF16T,))
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[3] != d or k_pages.shape[1] != Hkv:
+def _pages(dev: int, k_pages, v_pages, Hkv: int, d: int):
+    shape = k_pages.shape
+    if len(shape) != 4 or shape != v_pages.shape or shape[3] != d or shape[1] != Hkv:
         raise ValueError("k_pages and v_pages must be [n_pages, Hkv, page_size, d]")
-    return k_pages.shape[0], k_pages.shape[2]
+    n = k_pages.numel()
+    return shape[0], shape[2], _arg(dev, "k_pages", k_pages, _BF16T, n), _arg(dev, "v_pages", v_pages, _BF16T, n)
 
 
 def rope_paged_append(q, k, v, positions, slots, theta: float, k_pages, v_pages, q_rot=None, stream=None) -> torch.Tensor:
@@ -503,32 +520,26 @@ def rope_paged_append(q, k, v, positions, slots, theta: float, k_pages, v_pages,
     slot are skipped."""
     dev = _current(q, "q")
     T, Hq, d = q.shape
-    Hkv = k.shape[1]
-    for t, nm in ((q, "q"), (k, "k"), (v, "v")):
-        _same_device(dev, nm, t, (_BF16T, _F32T))
-        if t.dtype != q.dtype:
-            raise ValueError("q, k and v must have one type")
+    Hkv, dt, xt = k.shape[1], q.dtype, _float_code("q", q)
     if k.shape != (T, Hkv, d) or v.shape != k.shape:
         raise ValueError("k and v must be [T, Hkv, d]")
-    for t, nm in ((positions, "positions"), (slots, "slots")):
-        _same_device(dev, nm, t, (_I32,))
-        if t.numel() != T:
-            raise ValueError(f"{nm} must have {T} entries")
-    n_pages, P = _pages(dev, k_pages, v_pages, Hkv, d)
+    n_pages, P, kp, vp = _pages(dev, k_pages, v_pages, Hkv, d)
     if q_rot is None:
-        q_rot = torch.empty(T, Hq, d, dtype=_BF16T, device=dev)
-    else:
-        _same_device(dev, "q_rot", q_rot, (_BF16T,))
-        if q_rot.shape != q.shape:
-            raise ValueError("q_rot must have the shape of q")
-    _check(lib().bitnet_rope_paged_append(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q.dtype), T, Hq, Hkv, d, _ptr(positions),
-                                          _ptr(slots), float(theta), _ptr(q_rot), _ptr(k_pages), _ptr(v_pages), n_pages,
-                                          P, _stream(stream)), "rope_paged_append")
+        q_rot = _empty_strided_cuda((T, Hq, d), (Hq * d, d, 1), _BF16T)
+    elif q_rot.shape != q.shape:
+        raise ValueError("q_rot must have the shape of q")
+    n, nk = T * Hq * d, T * Hkv * d
+    st = lib().bitnet_rope_paged_append(
+        _arg(dev, "q", q, dt, n), _arg(dev, "k", k, dt, nk), _arg(dev, "v", v, dt, nk), xt, T, Hq, Hkv, d,
+        _arg(dev, "positions", positions, _I32, T), _arg(dev, "slots", slots, _I32, T), theta,
+        _arg(dev, "q_rot", q_rot, _BF16T, n), kp, vp, n_pages, P, _stream(stream))
+    if st:
+        raise BitnetError(st, "rope_paged_append")
     return q_rot
 
 
 def attention_paged_workspace_bytes(Hq: int, Hkv: int, max_new: int) -> int:
-    return int(lib().bitnet_attention_paged_workspace_bytes(Hq, Hkv, max_new))
+    return lib().bitnet_attention_paged_workspace_bytes(Hq, Hkv, max_new)
 
 
 def attention_paged(q_rot, k_pages, v_pages, block_table, cu_new, kv_lens, max_new: int, out_dtype=torch.bfloat16,
@@ -539,27 +550,27 @@ def attention_paged(q_rot, k_pages, v_pages, block_table, cu_new, kv_lens, max_n
     dev = _current(q_rot, "q_rot")
     T, Hq, d = q_rot.shape
     B, width = block_table.shape
-    _same_device(dev, "q_rot", q_rot, (_BF16T,))
     Hkv = k_pages.shape[1]
-    n_pages, P = _pages(dev, k_pages, v_pages, Hkv, d)
-    for t, n, nm in ((block_table, B * width, "block_table"), (cu_new, B + 1, "cu_new"), (kv_lens, B, "kv_lens")):
-        _same_device(dev, nm, t, (_I32,))
-        if t.numel() != n:
-            raise ValueError(f"{nm} must have {n} entries")
+    n_pages, P, kp, vp = _pages(dev, k_pages, v_pages, Hkv, d)
+    n = T * Hq * d
     if out is None:
-        out = torch.empty(T, Hq, d, dtype=out_dtype, device=dev)
+        out = _empty_strided_cuda((T, Hq, d), (Hq * d, d, 1), out_dtype)
+        to = out.data_ptr()
     else:
-        _same_device(dev, "out", out, (_BF16T, _F32T))
         if out.shape != q_rot.shape:
             raise ValueError("out must have the shape of q_rot")
+        to = _arg(dev, "out", out, out.dtype, n)
     if ws is None:
-        ws = torch.empty(max(attention_paged_workspace_bytes(Hq, Hkv, max_new), 16), dtype=torch.uint8, device=dev)
+        nws = max(lib().bitnet_attention_paged_workspace_bytes(Hq, Hkv, max_new), 16)
+        ws = _empty_strided_cuda((nws,), (1,), torch.uint8)
     else:
-        _same_device(dev, "ws", ws, (torch.uint8,))
-    _check(lib().bitnet_attention_paged(_ptr(q_rot), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(cu_new),
-                                        _ptr(kv_lens), T, B, Hq, Hkv, d, n_pages, P, width, max_new, _ptr(out),
-                                        _dtype_code(out.dtype), _ptr(ws), ws.numel(), _stream(stream)),
-           "attention_paged")
+        nws = ws.numel()
+    st = lib().bitnet_attention_paged(
+        _arg(dev, "q_rot", q_rot, _BF16T, n), kp, vp, _arg(dev, "block_table", block_table, _I32, B * width),
+        _arg(dev, "cu_new", cu_new, _I32, B + 1), _arg(dev, "kv_lens", kv_lens, _I32, B), T, B, Hq, Hkv, d, n_pages, P, width,
+        max_new, to, _float_code("out", out), _arg(dev, "ws", ws, torch.uint8, nws), nws, _stream(stream))
+    if st:
+        raise BitnetError(st, "attention_paged")
     return out
 
 

@@ -49,8 +49,8 @@ BN_DEV float exp2_approx(float x) {
   return y;
 }
 
-// x / d for 0 <= x < 2^22, d <= 1024, m = ceil(2^32 / d): m d - 2^32 < d, so x m / 2^32 exceeds x / d by
-// less than x d / (2^32 d) < 1 / d.
+// x / d for x >= 0, x d < 2^32, m = ceil(2^32 / d): m d - 2^32 < d, so x m / 2^32 exceeds x / d by less
+// than x / 2^32 < 1 / d.
 BN_DEV int div_small(int x, uint64_t m) { return (int)(((uint64_t)(uint32_t)x * m) >> 32); }
 // a / b for non-negative numbers, most often of 32 bits (a 64-bit division takes several times as long).
 BN_DEV long long div_nonneg(long long a, long long b) {

@@ -1293,8 +1293,10 @@ bitnet_status bitnet_rope_paged_append(const void* q, const void* k, const void*
   for (const void* p : {q, k, v, (const void*)q_rot, (const void*)k_pages, (const void*)v_pages})
     if (!aligned16(p)) return BITNET_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(positions) & 3u) || (reinterpret_cast<uintptr_t>(slots) & 3u)) return BITNET_ERR_ALIGN;
-  RopeTurns turns;
-  for (int i = 0; i < PG_D / 2; ++i) turns.g[i] = std::pow(theta, -2.0 * i / PG_D) / 6.283185307179586476925;
+  RopeTurns turns;  // theta^(-2i/128) / (2 pi), the powers as products of 64 bits of significand: i roundings of 2^-64
+  const long double step = std::pow((long double)theta, -2.0L / PG_D);
+  long double g = 1.0L / 6.283185307179586476925286766559L;
+  for (int i = 0; i < PG_D / 2; ++i, g *= step) turns.g[i] = (double)g;
   const dim3 grid((unsigned)((T + ROPE_TOKENS - 1) / ROPE_TOKENS)), block(ROPE_THREADS);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   __nv_bfloat16 *qo = reinterpret_cast<__nv_bfloat16*>(q_rot), *ko = reinterpret_cast<__nv_bfloat16*>(k_pages),
