@@ -137,12 +137,12 @@ static bitnet_status enqueue_quant(const void* x, bitnet_dtype xt, const float* 
       auto* kern = w == 1 ? k_rmsnorm_quant_warps<__nv_bfloat16, 1>
                           : (w == 2 ? k_rmsnorm_quant_warps<__nv_bfloat16, 2> : k_rmsnorm_quant_warps<__nv_bfloat16, 4>);
       e = launch(kern, dim3(grid), dim3(QW_THREADS), 0, s, true, reinterpret_cast<const __nv_bfloat16*>(x), gain, eps,
-                 (int)T, (int)K, q, s_x, sum_q, (const void*)nullptr, (void*)nullptr);
+                 (int)T, (int)K, q, s_x, sum_q);
     } else {
       auto* kern = w == 1 ? k_rmsnorm_quant_warps<float, 1>
                           : (w == 2 ? k_rmsnorm_quant_warps<float, 2> : k_rmsnorm_quant_warps<float, 4>);
       e = launch(kern, dim3(grid), dim3(QW_THREADS), 0, s, true, reinterpret_cast<const float*>(x), gain, eps, (int)T,
-                 (int)K, q, s_x, sum_q, (const void*)nullptr, (void*)nullptr);
+                 (int)K, q, s_x, sum_q);
     }
     if (e != cudaSuccess) return cuda_fail(e, "k_rmsnorm_quant_warps");
     return BITNET_OK;
@@ -172,7 +172,7 @@ static bitnet_status enqueue_quant(const void* x, bitnet_dtype xt, const float* 
   const size_t esz = xt == BITNET_BF16 ? 2 : 4;
   const int vec = (K % 8 == 0) && aligned16(x) && aligned16(q) && ((K * esz) % 16 == 0);
   cudaError_t e;
-  if (smem > 48 * 1024) {
+  if (smem > 47 * 1024) {  // 48 KB without opting in, of which the kernels' static memory takes some
     // Opt in to the large dynamic shared memory once per device and kernel.
     static std::atomic<int> done_mask[2][64] = {};
     int dev = 0;
@@ -200,8 +200,23 @@ static bitnet_status enqueue_quant(const void* x, bitnet_dtype xt, const float* 
   return BITNET_OK;
 }
 
-// Residual addition in front of the norm: the same choice of kernel as enqueue_quant, without the
-// double-buffered one for long fp32 rows (a residual stream is a model's hidden width).
+// Residual addition in front of the norm.  Rows that fit 16 warps' registers: 32 values a thread
+// with many rows, 8 (with up to eight warps) where there are too few rows to fill the GPU and a
+// row's own latency counts.  Longer rows go by way of shared memory.
+template <typename TIn, typename TRes, bool ALIGNED>
+static cudaError_t launch_add_quant(const TIn* x, const TRes* r_in, TRes* r_out, const float* gain, float eps, int64_t T, int64_t K,
+                                    int8_t* q, float* s_x, int32_t* sum_q, cudaStream_t s) {
+  const int64_t places = K + (ALIGNED ? 0 : 7), per_warp = T <= 256 ? 256 : 1024;
+  const int w = places <= per_warp ? 1 : (places <= 2 * per_warp ? 2 : (places <= 4 * per_warp ? 4 : (places <= 8 * 1024 ? 8 : 16)));
+  const int threads = qw_threads(w), rows = threads / 32 / w;
+  auto* kern = w == 1   ? k_add_rmsnorm_quant<TIn, TRes, 1, ALIGNED>
+               : w == 2 ? k_add_rmsnorm_quant<TIn, TRes, 2, ALIGNED>
+               : w == 4 ? k_add_rmsnorm_quant<TIn, TRes, 4, ALIGNED>
+               : w == 8 ? k_add_rmsnorm_quant<TIn, TRes, 8, ALIGNED>
+                        : k_add_rmsnorm_quant<TIn, TRes, 16, ALIGNED>;
+  return launch(kern, dim3((unsigned)((T + rows - 1) / rows)), dim3((unsigned)threads), 0, s, true, x, gain, eps, (int)T, (int)K, q, s_x,
+                sum_q, r_in, r_out);
+}
 template <typename TIn, typename TRes>
 static bitnet_status enqueue_add_quant(const void* x, const void* r_in, void* r_out, const float* gain, float eps,
                                        int64_t T, int64_t K, int8_t* q, float* s_x, int32_t* sum_q, cudaStream_t s) {
@@ -209,20 +224,16 @@ static bitnet_status enqueue_add_quant(const void* x, const void* r_in, void* r_
   const TRes* rp = reinterpret_cast<const TRes*>(r_in);
   TRes* op = reinterpret_cast<TRes*>(r_out);
   cudaError_t e;
-  if (K <= 4 * 2048 && K % 8 == 0) {  // every row 16-byte aligned in all three types
-    const int w = (T <= 256 || K > 4096) ? 4 : (K <= 2048 ? 1 : 2);
-    const int rows = QW_THREADS / 32 / w;
-    auto* kern = w == 1 ? k_rmsnorm_quant_warps<TIn, 1, TRes>
-                        : (w == 2 ? k_rmsnorm_quant_warps<TIn, 2, TRes> : k_rmsnorm_quant_warps<TIn, 4, TRes>);
-    e = launch(kern, dim3((unsigned)((T + rows - 1) / rows)), dim3(QW_THREADS), 0, s, true, xp, gain, eps, (int)T,
-               (int)K, q, s_x, sum_q, rp, op);
-    return e == cudaSuccess ? BITNET_OK : cuda_fail(e, "k_rmsnorm_quant_warps (residual)");
+  if (K + (K % 8 == 0 ? 0 : 7) <= 16 * 1024) {
+    e = K % 8 == 0 ? launch_add_quant<TIn, TRes, true>(xp, rp, op, gain, eps, T, K, q, s_x, sum_q, s)
+                   : launch_add_quant<TIn, TRes, false>(xp, rp, op, gain, eps, T, K, q, s_x, sum_q, s);
+    return e == cudaSuccess ? BITNET_OK : cuda_fail(e, "k_add_rmsnorm_quant");
   }
   int threads = (int)((K / 8 + 31) / 32 * 32);
   threads = threads < 128 ? 128 : (threads > 1024 ? 1024 : threads);
   const size_t smem = (size_t)K * sizeof(float);
   auto* kern = k_rmsnorm_quant<TIn, TRes>;
-  if (smem > 48 * 1024) {
+  if (smem > 47 * 1024) {  // 48 KB without opting in, of which the kernel's static memory takes some
     static std::atomic<int> done_dev[64] = {};  // one set per instance of this template
     int dev = 0;
     cudaGetDevice(&dev);
@@ -1297,20 +1308,20 @@ bitnet_status bitnet_rope_paged_append(const void* q, const void* k, const void*
   const long double step = std::pow((long double)theta, -2.0L / PG_D);
   long double g = 1.0L / 6.283185307179586476925286766559L;
   for (int i = 0; i < PG_D / 2; ++i, g *= step) turns.g[i] = (double)g;
-  const dim3 grid((unsigned)((T + ROPE_TOKENS - 1) / ROPE_TOKENS)), block(ROPE_THREADS);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  __nv_bfloat16 *qo = reinterpret_cast<__nv_bfloat16*>(q_rot), *ko = reinterpret_cast<__nv_bfloat16*>(k_pages),
-                *vo = reinterpret_cast<__nv_bfloat16*>(v_pages);
-  cudaError_t e;
-  if (xt == BITNET_BF16) {
-    typedef const __nv_bfloat16* P;
-    e = launch(k_rope_paged<__nv_bfloat16>, grid, block, 0, s, true, (P)q, (P)k, (P)v, positions, slots, (int)T, (int)Hq,
-               (int)Hkv, (int)page_size, (long long)(n_pages * page_size), turns, qo, ko, vo);
-  } else {
-    typedef const float* P;
-    e = launch(k_rope_paged<float>, grid, block, 0, s, true, (P)q, (P)k, (P)v, positions, slots, (int)T, (int)Hq,
-               (int)Hkv, (int)page_size, (long long)(n_pages * page_size), turns, qo, ko, vo);
-  }
+  // four tokens per CTA once that still gives every SM two CTAs
+  const int tok = T >= 8 * device_sm_count() ? 4 : 1;
+  auto run = [&](auto* x, auto* kern) {
+    typedef decltype(x) P;
+    return launch(kern, dim3((unsigned)((T + tok - 1) / tok)), dim3(ROPE_THREADS), 0, s, true, (P)q, (P)k, (P)v, positions, slots, (int)T,
+                  (int)Hq, (int)Hkv, page_log2(page_size), (long long)(n_pages * page_size), turns,
+                  reinterpret_cast<__nv_bfloat16*>(q_rot), reinterpret_cast<__nv_bfloat16*>(k_pages),
+                  reinterpret_cast<__nv_bfloat16*>(v_pages));
+  };
+  const __nv_bfloat16* xb = nullptr;
+  const float* xf = nullptr;
+  const cudaError_t e = xt == BITNET_BF16 ? (tok == 4 ? run(xb, k_rope_paged<__nv_bfloat16, 4>) : run(xb, k_rope_paged<__nv_bfloat16, 1>))
+                                          : (tok == 4 ? run(xf, k_rope_paged<float, 4>) : run(xf, k_rope_paged<float, 1>));
   return e == cudaSuccess ? BITNET_OK : cuda_fail(e, "k_rope_paged");
 }
 

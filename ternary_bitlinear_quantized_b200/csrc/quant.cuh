@@ -52,11 +52,32 @@ struct RowLoader<float> {
   BN_DEV static float load1(const float* p) { return *p; }
 };
 
-// v[0..8) = the stored residual TRes(v + r_in[0..8)).
-template <typename TRes>
-BN_DEV void add_residual8(float* v, const TRes* r_in, TRes* r_out) {
+// Eight values as they lie in memory.  The loads of a row's pieces are issued before the first one is
+// used: between them stand stores to r_out, which may be r_in, so the compiler keeps their order.
+template <typename T>
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+  BN_DEV void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  BN_DEV void get(float (&o)[8]) const {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 4)
+        o[i] = __uint_as_float(u[i]);
+      else
+        o[i] = __uint_as_float(i & 1 ? u[i >> 1] & 0xFFFF0000u : u[i >> 1] << 16);
+    }
+  }
+};
+// v[0..8) = the stored residual TRes(x + r), also written to r_out.
+template <typename TIn, typename TRes>
+BN_DEV void add_residual8(float (&v)[8], const Raw8<TIn>& x, const Raw8<TRes>& res, TRes* r_out) {
   float r[8];
-  RowLoader<TRes>::load(r_in, r);
+  x.get(v);
+  res.get(r);
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __fadd_rn(v[i], r[i]);
   if constexpr (std::is_same<TRes, float>::value) {
@@ -74,18 +95,15 @@ BN_DEV void add_residual8(float* v, const TRes* r_in, TRes* r_out) {
     *reinterpret_cast<uint4*>(r_out) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
-// The same for one value.
-template <typename TRes>
-BN_DEV float add_residual1(float v, const TRes* r_in, TRes* r_out) {
-  v = __fadd_rn(v, RowLoader<TRes>::load1(r_in));
-  if constexpr (std::is_same<TRes, float>::value) {
-    *r_out = v;
-    return v;
-  } else {
-    const __nv_bfloat16 b = __float2bfloat16_rn(v);
-    *r_out = b;
-    return __bfloat162float(b);
-  }
+// Stores v as a residual; the value as stored.
+BN_DEV float store_residual1(float v, float* out) {
+  *out = v;
+  return v;
+}
+BN_DEV float store_residual1(float v, __nv_bfloat16* out) {
+  const __nv_bfloat16 b = __float2bfloat16_rn(v);
+  *out = b;
+  return __bfloat162float(b);
 }
 
 // Quantise one staged row xs[0..K) in place of nothing: writes q, s_x, sum_q of the row.
@@ -165,8 +183,15 @@ BN_DEV float stage_row(const TIn* x, int K, float* xs, bool vec, void* red_scrat
   if (vec) {
     for (int k = tid * 8; k < K; k += nt * 8) {
       float v[8];
-      RowLoader<TIn>::load(x + k, v);
-      if constexpr (!std::is_void<TRes>::value) add_residual8<TRes>(v, r_in + k, r_out + k);
+      if constexpr (std::is_void<TRes>::value) {
+        RowLoader<TIn>::load(x + k, v);
+      } else {
+        Raw8<TIn> rx;
+        Raw8<TRes> rr;
+        rx.load(x + k);
+        rr.load(r_in + k);
+        add_residual8(v, rx, rr, r_out + k);
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         xs[k + j] = v[j];
@@ -174,11 +199,30 @@ BN_DEV float stage_row(const TIn* x, int K, float* xs, bool vec, void* red_scrat
       }
     }
   } else {
-    for (int k = tid; k < K; k += nt) {
-      float v = RowLoader<TIn>::load1(x + k);
-      if constexpr (!std::is_void<TRes>::value) v = add_residual1<TRes>(v, r_in + k, r_out + k);
-      xs[k] = v;
-      am = fmaxf(am, fabsf(v));
+    if constexpr (std::is_void<TRes>::value) {
+      for (int k = tid; k < K; k += nt) {
+        const float v = RowLoader<TIn>::load1(x + k);
+        xs[k] = v;
+        am = fmaxf(am, fabsf(v));
+      }
+    } else {
+      for (int k0 = tid; k0 < K; k0 += 8 * nt) {  // eight loads in flight, see Raw8
+        float v[8], r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int k = k0 + i * nt;
+          v[i] = k < K ? RowLoader<TIn>::load1(x + k) : 0.0f;
+          r[i] = k < K ? RowLoader<TRes>::load1(r_in + k) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int k = k0 + i * nt;
+          if (k < K) {
+            xs[k] = v[i] = store_residual1(__fadd_rn(v[i], r[i]), r_out + k);
+            am = fmaxf(am, fabsf(v[i]));
+          }
+        }
+      }
     }
   }
   return block_reduce(am, reinterpret_cast<float*>(red_scratch), MaxOp());
@@ -405,12 +449,11 @@ BN_DEV T qw_reduce(T v, T* slots, int& flip, int bar_id, int rank, Op op) {
   return r;
 }
 
-template <typename TIn, int W, typename TRes = void>
+template <typename TIn, int W>
 __global__ void __launch_bounds__(QW_THREADS) k_rmsnorm_quant_warps(const TIn* __restrict__ x,
                                                                    const float* __restrict__ gain, float eps, int T,
                                                                    int K, int8_t* __restrict__ q,
-                                                                   float* __restrict__ s_x, int32_t* __restrict__ sum_q,
-                                                                   const TRes* r_in, TRes* r_out) {
+                                                                   float* __restrict__ s_x, int32_t* __restrict__ sum_q) {
   constexpr int ROWS = QW_THREADS / 32 / W;
   __shared__ float redf[ROWS][2 * W];
   __shared__ long long redl[ROWS][2 * W];
@@ -431,7 +474,6 @@ __global__ void __launch_bounds__(QW_THREADS) k_rmsnorm_quant_warps(const TIn* _
     const int k = 8 * (lane + 32 * (rank + W * j));
     if (k < K) {
       RowLoader<TIn>::load(xr + k, v[j]);
-      if constexpr (!std::is_void<TRes>::value) add_residual8<TRes>(v[j], r_in + t * K + k, r_out + t * K + k);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
@@ -501,6 +543,195 @@ __global__ void __launch_bounds__(QW_THREADS) k_rmsnorm_quant_warps(const TIn* _
     }
   }
   sum = qw_reduce<W>(sum, &redi[rr][0], fi, bar, rank, AddOpI());
+  if (rank == 0 && lane == 0) {
+    s_x[t] = s;
+    sum_q[t] = sum;
+  }
+}
+
+// Residual addition + norm + codes (see the top of the file) for rows of up to 1024 W values: W warps
+// per row, 32 values a thread in registers, eight consecutive ones at a time.  ALIGNED: K is a
+// multiple of 8.  Otherwise the groups of eight are those of the whole tensor, on which its 16-byte
+// boundaries lie: a row begins `off` values into its first group and takes K + off <= 1024 W places; its
+// first and last group, where not whole, are read and written value by value.
+//
+// Bound by HBM if enough loads are in flight: all of a thread's loads stand before its first store
+// (r_out may be r_in, so the compiler keeps their order), and 32 values a thread leave room for 24 or 32
+// warps an SM.  Then the instructions count: the terms of the sum are one fused multiply-add each with
+// the rounding offset taken off once, codes and their sum come from the bits of the rounding addition
+// (as in k_rmsnorm_quant_long), and additions and products are done two at a time.
+// T = K = 8192, bf16: 150 us with 64 values a thread and one load, add and store after the other,
+// 94 us with the loads first and 32 values, 82 us (5.7 TB/s) as it stands.
+// Values behind the row are 0: their terms and codes are those of 0 and cancel with the offsets.
+// Pairs of fp32 in one 64-bit register, one instruction for both.
+BN_DEV uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+BN_DEV void halves(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+BN_DEV uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+BN_DEV uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+BN_HOST_DEV constexpr int qw_threads(int W) { return W > 8 ? 32 * W : QW_THREADS; }
+template <typename TIn, typename TRes, int W, bool ALIGNED>
+__global__ void __launch_bounds__(qw_threads(W), W > 8 ? 2 : (ALIGNED && sizeof(TIn) + sizeof(TRes) < 8 ? 4 : 3)) k_add_rmsnorm_quant(const TIn* __restrict__ x, const float* __restrict__ gain, float eps,
+                                                                  int T, int K, int8_t* __restrict__ q, float* __restrict__ s_x,
+                                                                  int32_t* __restrict__ sum_q, const TRes* r_in, TRes* r_out) {
+  constexpr int ROWS = qw_threads(W) / 32 / W, N = 32;
+  __shared__ float redf[ROWS][2 * W];
+  __shared__ long long redl[ROWS][2 * W];
+  __shared__ int redi[ROWS][2 * W];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rr = warp / W, rank = warp - rr * W;
+  const long long t = (long long)blockIdx.x * ROWS + rr;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (t >= T) return;  // every warp of the row leaves together
+  const int bar = 1 + rr;
+  int ff = 0, fl = 0, fi = 0;
+  const int off = ALIGNED ? 0 : (int)((t * K) & 7);
+  auto at = [&](int j) { return 8 * (lane + 32 * (rank + W * j)) - off; };  // first value of this thread's group j
+  auto whole = [&](int j) { return ALIGNED ? at(j) < K : at(j) >= 0 && at(j) + 8 <= K; };
+  auto has = [&](int j, int i) { return (unsigned)(at(j) + i) < (unsigned)K; };
+  auto any = [&](int j) { return 256 * (rank + W * j) - off < K; };  // whether the warp has any of them
+  uint64_t v[N / 2];
+  {
+    Raw8<TIn> rx[N / 8];
+    Raw8<TRes> rr8[N / 8];
+#pragma unroll
+    for (int j = 0; j < N / 8; ++j)
+      if (whole(j)) {
+        rx[j].load(x + t * K + at(j));
+        rr8[j].load(r_in + t * K + at(j));
+      }
+#pragma unroll
+    for (int j = 0; j < N / 8; ++j) {
+      float o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      if (whole(j)) {
+        add_residual8(o, rx[j], rr8[j], r_out + t * K + at(j));
+      } else if (!ALIGNED) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const long long at1 = t * K + at(j) + i;
+          if (has(j, i)) o[i] = store_residual1(__fadd_rn(RowLoader<TIn>::load1(x + at1), RowLoader<TRes>::load1(r_in + at1)), r_out + at1);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * j + i] = pair(o[2 * i], o[2 * i + 1]);
+    }
+  }
+  float am = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    float lo, hi;
+    halves(v[i], lo, hi);
+    am = fmaxf(fmaxf(am, fabsf(lo)), fabsf(hi));
+  }
+  am = qw_reduce<W>(am, &redf[rr][0], ff, bar, rank, MaxOp());
+  float a = am;
+  uint64_t seen = 0ull;  // sums of this thread's y: finite only if every one of them is
+  if (gain != nullptr) {
+    float ms = 0.0f;
+    if (am > 0.0f) {
+      const int e = fixed_point_exponent(__dmul_rn((double)am, (double)am), K);
+      const double p2e = pow2_f64(e);
+      unsigned long long bits = 0ull;
+#pragma unroll
+      for (int j = 0; j < N / 8; ++j) {
+        if (!any(j)) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float lo, hi;
+          halves(v[4 * j + i], lo, hi);
+          if (K >= kFixedSmallMinN) {
+            const double d0 = (double)lo, d1 = (double)hi;
+            bits += (unsigned long long)__double_as_longlong(__fma_rn(d0, __dmul_rn(d0, p2e), 6755399441055744.0)) +
+                    (unsigned long long)__double_as_longlong(__fma_rn(d1, __dmul_rn(d1, p2e), 6755399441055744.0));
+          } else {
+            bits += (unsigned long long)(fixed_sq_term(lo, p2e) + fixed_sq_term(hi, p2e));
+          }
+        }
+        if (K >= kFixedSmallMinN) bits -= 8 * 0x4338000000000000ull;
+      }
+      ms = fixed_point_mean(qw_reduce<W>((long long)bits, &redl[rr][0], fl, bar, rank, AddOpLL()), e, K);
+    }
+    const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, eps)));
+    const uint64_t inv2 = pair(inv, inv);
+    float ay = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N / 8; ++j) {
+      if (!any(j)) continue;
+      uint64_t g[4];
+      if constexpr (ALIGNED) {
+        const ulonglong2* p = reinterpret_cast<const ulonglong2*>(gain + (at(j) < K ? at(j) : 0));
+        const ulonglong2 g0 = __ldg(p), g1 = __ldg(p + 1);
+        g[0] = g0.x, g[1] = g0.y, g[2] = g1.x, g[3] = g1.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          g[i] = pair(__ldg(gain + (has(j, 2 * i) ? at(j) + 2 * i : 0)), __ldg(gain + (has(j, 2 * i + 1) ? at(j) + 2 * i + 1 : 0)));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint64_t& y = v[4 * j + i];
+        y = mul_pair(mul_pair(y, inv2), g[i]);
+        seen = add_pair(seen, y);
+        float lo, hi;
+        halves(y, lo, hi);
+        ay = fmaxf(fmaxf(ay, fabsf(lo)), fabsf(hi));
+      }
+    }
+    a = qw_reduce<W>(ay, &redf[rr][0], ff, bar, rank, MaxOp());
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) seen = add_pair(seen, v[i]);
+  }
+  // |y| <= a for every number y, so |y s| rounds to at most 127 and needs no clamp; what does need it
+  // is a NaN or an infinity, which the sum shows.
+  const float s = __fdiv_rn(127.0f, fmaxf(a, 1e-5f));
+  const uint64_t s2 = pair(s, s), round2 = pair(12582912.0f, 12582912.0f);
+  float slo, shi;
+  halves(seen, slo, shi);
+  const bool finite = fabsf(__fadd_rn(slo, shi)) < INFINITY;
+  uint32_t cbits = 0;
+  int8_t* qr = q + t * K;
+#pragma unroll
+  for (int j = 0; j < N / 8; ++j) {
+    if (!any(j)) continue;
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint64_t p = mul_pair(v[4 * j + i], s2);
+      float lo, hi;
+      if (!finite) {
+        halves(p, lo, hi);
+        p = pair(lo == lo ? fminf(fmaxf(lo, -128.0f), 127.0f) : 0.0f, hi == hi ? fminf(fmaxf(hi, -128.0f), 127.0f) : 0.0f);
+      }
+      halves(add_pair(p, round2), lo, hi);
+      b[2 * i] = __float_as_uint(lo);
+      b[2 * i + 1] = __float_as_uint(hi);
+      cbits += b[2 * i] + b[2 * i + 1];
+    }
+    cbits -= 8 * 0x4B400000u;
+    if (whole(j)) {
+      *reinterpret_cast<uint2*>(qr + at(j)) =
+          make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                     __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+    } else if (!ALIGNED) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (has(j, i)) qr[at(j) + i] = (int8_t)b[i];
+    }
+  }
+  const int sum = qw_reduce<W>((int)cbits, &redi[rr][0], fi, bar, rank, AddOpI());
   if (rank == 0 && lane == 0) {
     s_x[t] = s;
     sum_q[t] = sum;

@@ -104,7 +104,8 @@ def test_plan_flags_lengths_out_of_range():
 # ------------------------------------------------------------------------------------------- norm
 
 @pytest.mark.parametrize("T,K", [(1, 1), (3, 7), (2, 57), (5, 128), (1, 2560), (300, 640), (7, 5120), (4, 8192), (3, 8200),
-                                 (2, 12289), (2, 49152), (257, 2048)])
+                                 (2, 12289), (2, 49152), (257, 2048),
+                                 (3, 12288), (300, 1023), (300, 1025), (600, 3001), (2, 8191), (300, 8185), (300, 8186), (3, 16377), (3, 16378), (2, 16384), (9, 249), (9, 250)])
 @pytest.mark.parametrize("xt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rt", [torch.bfloat16, torch.float32])
 def test_add_rmsnorm_quant_act(T, K, xt, rt):
@@ -118,6 +119,16 @@ def test_add_rmsnorm_quant_act(T, K, xt, rt):
         assert torch.equal(res.cpu(), want)
         oq, os_, osq = O.rmsnorm_quant_act(act_to_np(want), None if gn is None else gn.numpy(), 1e-6)
         assert np.array_equal(q.cpu().numpy(), oq) and np.array_equal(s.cpu().numpy(), os_) and np.array_equal(sq.cpu().numpy(), osq)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K", [12224, 12288, 12296])
+def test_rmsnorm_quant_act_rows_of_48_kb(K, dt):
+    """A row of 48 KB in shared memory, beside the kernel's own few bytes."""
+    x = torch.randn(3, K, generator=torch.Generator().manual_seed(K)).to(dt)
+    q, s, sq = tb.rmsnorm_quant_act(x.to(DEV), None)
+    oq, os_, osq = O.rmsnorm_quant_act(act_to_np(x), None, 1e-6)
+    assert np.array_equal(q.cpu().numpy(), oq) and np.array_equal(s.cpu().numpy(), os_) and np.array_equal(sq.cpu().numpy(), osq)
 
 
 def test_add_rmsnorm_quant_act_in_place_and_zero_rows():
@@ -134,10 +145,33 @@ def test_add_rmsnorm_quant_act_in_place_and_zero_rows():
     assert tb.add_rmsnorm_quant_act(x[:0], r[:0], None)[0].shape == (0, 640)
 
 
+@pytest.mark.parametrize("K", [640, 2047, 5120, 8200])
+def test_add_rmsnorm_quant_act_non_finite(K):
+    """Rows with NaN and infinities, large sums, an infinite or NaN gain and eps = 0 on a zero row: what rmsnorm_quant_act
+    gives for the same stream."""
+    g = torch.Generator().manual_seed(K)
+    x = torch.zeros(9, K)
+    r = torch.randn(9, K, generator=g)
+    r[0, 3], r[1, 5], r[2, 7] = float("nan"), float("inf"), -float("inf")
+    r[3, 1], r[3, 2] = float("inf"), -float("inf")
+    r[4] = 3e38
+    r[5] = 0
+    gain = 1.0 + 0.1 * torch.randn(K, generator=g)
+    odd = gain.clone()
+    odd[2], odd[4] = float("inf"), float("nan")
+    for gn, eps in ((gain, 1e-6), (odd, 1e-6), (gain, 0.0), (None, 1e-6)):
+        gd = None if gn is None else gn.to(DEV)
+        res, *got = tb.add_rmsnorm_quant_act(x.to(DEV), r.to(DEV), gd, eps)
+        assert torch.equal(torch.nan_to_num(res), torch.nan_to_num(r.to(DEV)))
+        for a, b in zip(got, tb.rmsnorm_quant_act(res, gd, eps)):
+            assert torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b.float()))
+
+
 # ------------------------------------------------------------------------------------------- rope
 
 @pytest.mark.parametrize("T,Hq,Hkv,P,theta", [(1, 20, 5, 16, 10000.0), (4, 64, 8, 32, 500000.0), (5, 8, 8, 256, 10000.0),
-                                              (37, 12, 4, 64, 10000.0), (130, 16, 1, 128, 500000.0)])
+                                              (37, 12, 4, 64, 10000.0), (130, 16, 1, 128, 500000.0),
+                                              (1701, 20, 5, 32, 10000.0)])
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 def test_rope_paged_append(T, Hq, Hkv, P, theta, dt):
     g = torch.Generator().manual_seed(T)
