@@ -604,19 +604,21 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
   }
 }
 
-// Thread: a row and 16 of its dimensions (blockIdx.y).
+// Thread: a row and PC_JOIN_V4 float4 of its dimensions (blockIdx.y).
+constexpr int PC_JOIN_V4 = 2;
 __global__ void __launch_bounds__(PC_M) k_attn_paged_chunk_join(const PagedArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   const PagedTile d = a.desc[blockIdx.x];
   if (d.first < 0) return;
-  const int row = threadIdx.x, g0 = blockIdx.y * 4;
+  const int row = threadIdx.x, g0 = blockIdx.y * PC_JOIN_V4;
   const ChunkRow r = chunk_row(a, d.n, d.tile, row);
   if (!r.there) return;
-  float o[16], l;
-  join_parts<4>(a.part, PC_PART, PC_M * PG_D, PC_M, row, d.first, blockIdx.x, PG_SCALE_LOG2, [&](int k) { return ((g0 + k) * PC_M + row) * 4; },
-                o, l);
-  store_row<4>(a.out, a.out_dtype, ((long long)(d.t0 + r.t) * a.Hq + d.head * a.G + r.g) * PG_D + g0 * 4, o);
+  float o[4 * PC_JOIN_V4], m, l;
+  join_parts<PC_JOIN_V4>(a.part, PC_PART, PC_M * PG_D, PC_M, row, d.first, d.first, 1, blockIdx.x, PG_SCALE_LOG2,
+                [&](int k) { return ((g0 + k) * PC_M + row) * 4; }, o, m, l);
+  divide_row(o, l);
+  store_row<PC_JOIN_V4>(a.out, a.out_dtype, ((long long)(d.t0 + r.t) * a.Hq + d.head * a.G + r.g) * PG_D + g0 * 4, o);
 }
 
 }  // namespace bitnet

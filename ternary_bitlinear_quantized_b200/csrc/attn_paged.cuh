@@ -512,23 +512,24 @@ __global__ void __launch_bounds__(PD_THREADS, 2) k_attn_paged_few(const PagedArg
 }
 
 // Joins the parts of the tile that CTA blockIdx.x ended: part 1 of the CTA that the tile began in, and
-// part 0 of every later one.  Each thread adds up V4 float4 of one row, four parts at a time so
-// that their loads are in flight together; `at(part, k)` is the place of the row's k-th one.
+// part 0 of every later one.  Each thread adds up V4 float4 of one row over the parts first,
+// first + step, ... four at a time so that their loads are in flight together; `at(part, k)` is the
+// place of the row's k-th one.
 template <int V4, typename At>
-BN_DEV void join_parts(const float* parts, int stride, int stats, int rows, int row, int first, int last, float scale_log2, At at,
-                       float (&o)[4 * V4], float& l) {
-  float m = -INFINITY;
+BN_DEV void join_parts(const float* parts, int stride, int stats, int rows, int row, int tile_first, int first, int step, int last,
+                       float scale_log2, At at, float (&o)[4 * V4], float& m, float& l) {
+  m = -INFINITY;
   l = 0.0f;
 #pragma unroll
   for (int k = 0; k < 4 * V4; ++k) o[k] = 0.0f;
-  for (int i0 = first; i0 <= last; i0 += 4) {
+  for (int i0 = first; i0 <= last; i0 += 4 * step) {
     float pm[4], pl[4];
     float4 x[4][V4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int i = min(i0 + u, last);
-      const float* p = parts + ((long long)i * 2 + (i == first ? 1 : 0)) * stride;
-      pm[u] = i0 + u <= last ? p[stats + row] : -INFINITY;
+      const int i = i0 + u * step <= last ? i0 + u * step : first;
+      const float* p = parts + ((long long)i * 2 + (i == tile_first ? 1 : 0)) * stride;
+      pm[u] = i0 + u * step <= last ? p[stats + row] : -INFINITY;  // weight 0 behind the last part
       pl[u] = p[stats + rows + row];
 #pragma unroll
       for (int k = 0; k < V4; ++k) x[u][k] = *reinterpret_cast<const float4*>(p + at(k));
@@ -542,7 +543,7 @@ BN_DEV void join_parts(const float* parts, int stride, int stats, int rows, int 
     for (int k = 0; k < 4 * V4; ++k) o[k] = __fmul_rn(o[k], old);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const float f = exp2_approx(__fmul_rn(__fsub_rn(pm[u], mu), scale_log2));  // 0 behind the last part
+      const float f = exp2_approx(__fmul_rn(__fsub_rn(pm[u], mu), scale_log2));
       l = __fmaf_rn(pl[u], f, l);
 #pragma unroll
       for (int k = 0; k < V4; ++k) {
@@ -553,9 +554,13 @@ BN_DEV void join_parts(const float* parts, int stride, int stats, int rows, int 
       }
     }
   }
+}
+// o / l, zero for a row that sees nothing.
+template <int N>
+BN_DEV void divide_row(float (&o)[N], float l) {
   const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);  // NaN stays
 #pragma unroll
-  for (int k = 0; k < 4 * V4; ++k) o[k] = __fmul_rn(o[k], inv);
+  for (int k = 0; k < N; ++k) o[k] = __fmul_rn(o[k], inv);
 }
 template <int V4>
 BN_DEV void store_row(void* out, int out_dtype, long long off, const float (&o)[4 * V4]) {
@@ -570,19 +575,53 @@ BN_DEV void store_row(void* out, int out_dtype, long long off, const float (&o)[
   }
 }
 
-// Thread: a row and eight of its dimensions.
-__global__ void __launch_bounds__(256) k_attn_paged_few_join(const PagedArgs a) {
+// A long cache with few rows leaves many parts to a tile, and their loads' latency is what counts:
+// a block takes PJ_ROWS rows, and PJ_GROUPS threads share the parts of four dimensions of a row, each
+// with four in flight.
+constexpr int PJ_ROWS = 8, PJ_GROUPS = 2;
+__global__ void __launch_bounds__(PJ_ROWS * 32 * PJ_GROUPS) k_attn_paged_few_join(const PagedArgs a) {
+  __shared__ float4 s_o[PJ_GROUPS - 1][PJ_ROWS][32];
+  __shared__ float s_m[PJ_GROUPS - 1][PJ_ROWS], s_l[PJ_GROUPS - 1][PJ_ROWS];
   pdl_launch_dependents();
   pdl_wait();
   const PagedTile d = a.desc[blockIdx.x];
   if (d.first < 0) return;
-  const int row = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * 8;
-  const int r = d.tile * PD_M + row;
-  if (r >= d.n * a.G) return;
-  float o[8], l;
-  join_parts<2>(a.part, PD_PART, PD_M * PG_D, PD_M, row, d.first, blockIdx.x, 1.0f, [&](int k) { return row * PG_D + d0 + 4 * k; }, o, l);
+  const int lane = threadIdx.x & 31, rr = (threadIdx.x >> 5) & (PJ_ROWS - 1), group = threadIdx.x / (32 * PJ_ROWS);
+  const int row = blockIdx.y * PJ_ROWS + rr, r = d.tile * PD_M + row;
+  if (d.tile * PD_M + blockIdx.y * PJ_ROWS >= d.n * a.G) return;
+  float o[4], m, l;
+  join_parts<1>(a.part, PD_PART, PD_M * PG_D, PD_M, row, d.first, d.first + group, PJ_GROUPS, blockIdx.x, 1.0f,
+                [&](int) { return row * PG_D + lane * 4; }, o, m, l);
+  if (group > 0) {
+    s_o[group - 1][rr][lane] = make_float4(o[0], o[1], o[2], o[3]);
+    if (lane == 0) {
+      s_m[group - 1][rr] = m;
+      s_l[group - 1][rr] = l;
+    }
+  }
+  __syncthreads();
+  if (group > 0 || r >= d.n * a.G) return;
+  float mn = m;
+#pragma unroll
+  for (int g = 0; g < PJ_GROUPS - 1; ++g) mn = fmaxf(mn, s_m[g][rr]);
+  const float mu = mn == -INFINITY ? 0.0f : mn;
+  const float f0 = exp2_approx(__fsub_rn(m, mu));
+  l = __fmul_rn(l, f0);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o[k] = __fmul_rn(o[k], f0);
+#pragma unroll
+  for (int g = 0; g < PJ_GROUPS - 1; ++g) {
+    const float f = exp2_approx(__fsub_rn(s_m[g][rr], mu));
+    const float4 x = s_o[g][rr][lane];
+    l = __fmaf_rn(s_l[g][rr], f, l);
+    o[0] = __fmaf_rn(x.x, f, o[0]);
+    o[1] = __fmaf_rn(x.y, f, o[1]);
+    o[2] = __fmaf_rn(x.z, f, o[2]);
+    o[3] = __fmaf_rn(x.w, f, o[3]);
+  }
+  divide_row(o, l);
   const int t = div_small(r, a.by_G);
-  store_row<2>(a.out, a.out_dtype, ((long long)(d.t0 + t) * a.Hq + d.head * a.G + (r - t * a.G)) * PG_D + d0, o);
+  store_row<1>(a.out, a.out_dtype, ((long long)(d.t0 + t) * a.Hq + d.head * a.G + (r - t * a.G)) * PG_D + lane * 4, o);
 }
 
 }  // namespace bitnet

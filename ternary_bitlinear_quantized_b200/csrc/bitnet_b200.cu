@@ -1409,7 +1409,7 @@ bitnet_status bitnet_attention_paged(const void* q_rot, const void* k_pages, con
     if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_few attribute");
     e = launch(k_attn_paged_few, dim3((unsigned)ctas), dim3(PD_THREADS), PD_RING, s, true, a);
     if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_few");
-    e = launch(k_attn_paged_few_join, dim3((unsigned)ctas), dim3(256), 0, s, true, a);
+    e = launch(k_attn_paged_few_join, dim3((unsigned)ctas, PD_M / PJ_ROWS), dim3(PJ_ROWS * 32 * PJ_GROUPS), 0, s, true, a);
     if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_few_join");
     return BITNET_OK;
   }
@@ -1423,7 +1423,7 @@ bitnet_status bitnet_attention_paged(const void* q_rot, const void* k_pages, con
   if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_chunk attribute");
   e = launch(k_attn_paged_chunk, dim3((unsigned)ctas), dim3(PC_THREADS), PC_SMEM, s, true, maps, a);
   if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_chunk");
-  e = launch(k_attn_paged_chunk_join, dim3((unsigned)ctas, PG_D / 16), dim3(PC_M), 0, s, true, a);
+  e = launch(k_attn_paged_chunk_join, dim3((unsigned)ctas, PG_D / (4 * PC_JOIN_V4)), dim3(PC_M), 0, s, true, a);
   if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_chunk_join");
   return BITNET_OK;
 }
