@@ -513,28 +513,35 @@ __global__ void __launch_bounds__(PD_THREADS, 2) k_attn_paged_few(const PagedArg
 
 // Joins the parts of the tile that CTA blockIdx.x ended: part 1 of the CTA that the tile began in, and
 // part 0 of every later one.  Each thread adds up V4 float4 of one row over the parts first,
-// first + step, ... four at a time so that their loads are in flight together; `at(part, k)` is the
+// first + step, ... BATCH at a time so that their loads are in flight together; `at(part, k)` is the
 // place of the row's k-th one.
-template <int V4, typename At>
+template <int V4, int BATCH, typename At>
 BN_DEV void join_parts(const float* parts, int stride, int stats, int rows, int row, int tile_first, int first, int step, int last,
                        float scale_log2, At at, float (&o)[4 * V4], float& m, float& l) {
   m = -INFINITY;
   l = 0.0f;
 #pragma unroll
   for (int k = 0; k < 4 * V4; ++k) o[k] = 0.0f;
-  for (int i0 = first; i0 <= last; i0 += 4 * step) {
-    float pm[4], pl[4];
-    float4 x[4][V4];
+  for (int i0 = first; i0 <= last; i0 += BATCH * step) {
+    float pm[BATCH], pl[BATCH], mn = m;
+    float4 x[BATCH][V4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = i0 + u * step <= last ? i0 + u * step : first;
-      const float* p = parts + ((long long)i * 2 + (i == tile_first ? 1 : 0)) * stride;
-      pm[u] = i0 + u * step <= last ? p[stats + row] : -INFINITY;  // weight 0 behind the last part
-      pl[u] = p[stats + rows + row];
+    for (int u = 0; u < BATCH; ++u) {
+      const int i = i0 + u * step;
+      pm[u] = -INFINITY;  // weight 0 behind the last part
+      pl[u] = 0.0f;
 #pragma unroll
-      for (int k = 0; k < V4; ++k) x[u][k] = *reinterpret_cast<const float4*>(p + at(k));
+      for (int k = 0; k < V4; ++k) x[u][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (i <= last) {
+        const float* p = parts + ((long long)i * 2 + (i == tile_first ? 1 : 0)) * stride;
+        pm[u] = p[stats + row];
+        pl[u] = p[stats + rows + row];
+#pragma unroll
+        for (int k = 0; k < V4; ++k) x[u][k] = *reinterpret_cast<const float4*>(p + at(k));
+      }
     }
-    const float mn = fmaxf(fmaxf(m, fmaxf(pm[0], pm[1])), fmaxf(pm[2], pm[3]));
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) mn = fmaxf(mn, pm[u]);
     const float mu = mn == -INFINITY ? 0.0f : mn;
     const float old = exp2_approx(__fmul_rn(__fsub_rn(m, mu), scale_log2));
     m = mn;
@@ -542,7 +549,7 @@ BN_DEV void join_parts(const float* parts, int stride, int stats, int rows, int 
 #pragma unroll
     for (int k = 0; k < 4 * V4; ++k) o[k] = __fmul_rn(o[k], old);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < BATCH; ++u) {
       const float f = exp2_approx(__fmul_rn(__fsub_rn(pm[u], mu), scale_log2));
       l = __fmaf_rn(pl[u], f, l);
 #pragma unroll
@@ -565,9 +572,17 @@ BN_DEV void divide_row(float (&o)[N], float l) {
 template <int V4>
 BN_DEV void store_row(void* out, int out_dtype, long long off, const float (&o)[4 * V4]) {
   if (out_dtype == BITNET_BF16) {
-    uint2* dst = reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out) + off);
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(out) + off;
+    if constexpr (V4 % 2 == 0) {
 #pragma unroll
-    for (int k = 0; k < V4; ++k) dst[k] = make_uint2(pack_bf16(o[4 * k], o[4 * k + 1]), pack_bf16(o[4 * k + 2], o[4 * k + 3]));
+      for (int k = 0; k < V4; k += 2)
+        reinterpret_cast<uint4*>(dst)[k / 2] = make_uint4(pack_bf16(o[4 * k], o[4 * k + 1]), pack_bf16(o[4 * k + 2], o[4 * k + 3]),
+                                                          pack_bf16(o[4 * k + 4], o[4 * k + 5]), pack_bf16(o[4 * k + 6], o[4 * k + 7]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < V4; ++k)
+        reinterpret_cast<uint2*>(dst)[k] = make_uint2(pack_bf16(o[4 * k], o[4 * k + 1]), pack_bf16(o[4 * k + 2], o[4 * k + 3]));
+    }
   } else {
     float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + off);
 #pragma unroll
@@ -590,7 +605,7 @@ __global__ void __launch_bounds__(PJ_ROWS * 32 * PJ_GROUPS) k_attn_paged_few_joi
   const int row = blockIdx.y * PJ_ROWS + rr, r = d.tile * PD_M + row;
   if (d.tile * PD_M + blockIdx.y * PJ_ROWS >= d.n * a.G) return;
   float o[4], m, l;
-  join_parts<1>(a.part, PD_PART, PD_M * PG_D, PD_M, row, d.first, d.first + group, PJ_GROUPS, blockIdx.x, 1.0f,
+  join_parts<1, 4>(a.part, PD_PART, PD_M * PG_D, PD_M, row, d.first, d.first + group, PJ_GROUPS, blockIdx.x, 1.0f,
                 [&](int) { return row * PG_D + lane * 4; }, o, m, l);
   if (group > 0) {
     s_o[group - 1][rr][lane] = make_float4(o[0], o[1], o[2], o[3]);

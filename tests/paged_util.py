@@ -101,6 +101,12 @@ def attention_ref(b: Batch):
     return out, bound, absum
 
 
+def weight_step(b: Batch) -> float:
+    """Half a step of the weights in the second product, as the call's documentation has it: two bf16 (2^-8 of 2^-8)
+    up to 32 query rows per request and key/value head, one bf16 above."""
+    return 2.0 ** -16 if b.max_new * (b.Hq // b.Hkv) <= 32 else 2.0 ** -8
+
+
 def check_attention(b: Batch, got: torch.Tensor, p_round: float = 2.0 ** -8, skip=()):
     """`skip`: requests that are not looked at.  `p_round`: rounding of a probability before the second product (a bf16's half step; 2^-16 where it enters
     as the sum of two bf16).  Rows behind the last request are not looked at."""

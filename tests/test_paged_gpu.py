@@ -8,7 +8,7 @@ import torch
 
 import ternary_bitlinear_quantized_b200 as tb
 from oracle import bitnet_oracle as O
-from tests.paged_util import D, Batch, attention_ref, check_attention, pages_of, plan_ref
+from tests.paged_util import D, Batch, attention_ref, check_attention, pages_of, plan_ref, weight_step
 from tests.parity_util import act_to_np
 
 pytestmark = pytest.mark.gpu
@@ -258,7 +258,9 @@ FEW = [
 def test_attention_few_rows(case, out_dtype):
     new, kv, Hq, Hkv, P = case
     b = Batch(new, kv, Hq, Hkv, P, seed=len(new), pad=2)
-    check_attention(b, _attend(b, out_dtype), p_round=2.0 ** -16)
+    # 33 rows of one token (the last case) take the kernel for many rows, whose weights are one bf16: by the definition
+    # o = sum w v / sum w, a half step of 2^-8 on each w moves o by at most 2^-8 sum w |v| / sum w
+    check_attention(b, _attend(b, out_dtype), p_round=weight_step(b))
     assert tb.device_status() == 0
 
 
