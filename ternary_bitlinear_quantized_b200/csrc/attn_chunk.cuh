@@ -5,8 +5,8 @@
 //                   tensor memory, maximum, weights (bf16) back to tensor memory; the output at the end
 //   warps 8, 9      one thread each, for the rows 0-127 and 128-255: tcgen05.mma S = Q K^T (both
 //                   operands in shared memory) and O += P V (P in tensor memory)
-//   warp 10         TMA loads of K, page by page, into a ring of two 32 KB slots, and of Q
-//   warp 11         TMA loads of V into another
+//   warp 10         TMA loads of K, page by page, into a ring of two 32 KB slots
+//   warp 11         TMA loads of Q, and of V into another ring
 // The two halves take turns: while one half's softmax runs, the tensor core does the other's
 // products.  Tensor memory (512 columns): S of each half 128 columns, of which P takes the first 64
 // once the scores are in registers; O of each half 128 columns.
@@ -99,6 +99,7 @@ BN_DEV void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t 
       ::"r"(d_tmem), "r"(a_tmem), "r"(b), "r"(accumulate), "n"(B_OFF), "r"(PC_DESC_HI), "r"(pc_idesc(128, true))
       : "memory");
 }
+BN_DEV void prefetch_map(const void* map) { asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory"); }
 BN_DEV void tma_load_4d(uint32_t dst, const void* map, int x, int y, int z, int w, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
@@ -251,6 +252,10 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
     s_abort = 0;
     s_issued[0] = s_issued[1] = s_q_issued = 0;
     fence_mbar_init();
+  }
+  if (warp >= PC_LOAD_WARP && lane == 0) {
+    prefetch_map(warp == PC_LOAD_WARP ? &maps.k : &maps.v);
+    if (warp != PC_LOAD_WARP) prefetch_map(&maps.q);
   }
   if (warp == PC_MMA_WARP) {
     tmem_alloc(smem_addr(&s_tmem), 512);
@@ -495,7 +500,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
       mbar_drain(mma_done, 0);
     }
   } else {
-    // ------------------------------------------------------------ K and Q (warp 10), V (warp 11)
+    // ------------------------------------------------------------ K (warp 10), Q and V (warp 11)
     const bool is_v = warp != PC_LOAD_WARP;
     const void* map = is_v ? &maps.v : &maps.k;
     const uint32_t buf = is_v ? sV : sK;
@@ -522,6 +527,23 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
           page = a.n_pages;
         }
         if (it + 1 < cnt) ahead = entry(w.unit + it + 1);
+        if (is_v && it == 0) {  // Q, which is needed before the first V
+          ok = warp_wait(q_empty, ph_q, &s_abort);
+          if (!ok) break;
+          ph_q ^= 1u;
+          if (elect_one()) {
+            const int nh = 2 * w.tile + 1 < w.blocks ? 2 : 1;
+            mbar_arrive_expect_tx(q_full, nh * a.TB * a.GB * PG_D * 2);
+            for (int h = 0; h < nh; ++h) {
+              const ChunkRow r = chunk_row(a, w.n, w.tile, h * 128);
+              const uint32_t dst = sQ + h * PC_TILE_BYTES;
+              tma_load_4d(dst, &maps.q, 0, r.g, w.head, w.t0 + r.t, q_full);
+              tma_load_4d(dst + 16384, &maps.q, 64, r.g, w.head, w.t0 + r.t, q_full);
+            }
+          }
+          __syncwarp();
+          ++q_issued;
+        }
         const uint32_t bar_full = is_v ? v_full(slot) : k_full(slot);
         ok = warp_wait(is_v ? v_empty(slot) : k_empty(slot), ph, &s_abort);
         if (!ok) break;
@@ -554,22 +576,6 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
             __syncwarp();
             if (lane == 0) mbar_arrive(v_fixed(slot));
           }
-        } else if (it == 0) {
-          ok = warp_wait(q_empty, ph_q, &s_abort);
-          if (!ok) break;
-          ph_q ^= 1u;
-          if (elect_one()) {
-            const int nh = 2 * w.tile + 1 < w.blocks ? 2 : 1;
-            mbar_arrive_expect_tx(q_full, nh * a.TB * a.GB * PG_D * 2);
-            for (int h = 0; h < nh; ++h) {
-              const ChunkRow r = chunk_row(a, w.n, w.tile, h * 128);
-              const uint32_t dst = sQ + h * PC_TILE_BYTES;
-              tma_load_4d(dst, &maps.q, 0, r.g, w.head, w.t0 + r.t, q_full);
-              tma_load_4d(dst + 16384, &maps.q, 64, r.g, w.head, w.t0 + r.t, q_full);
-            }
-          }
-          __syncwarp();
-          ++q_issued;
         }
         if (++slot == slots) {
           slot = 0;
@@ -580,7 +586,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
     if (!ok) s_abort = 1;
     if (lane == 0) {
       s_issued[is_v] = issued;
-      if (!is_v) s_q_issued = q_issued;
+      if (is_v) s_q_issued = q_issued;
     }
   }
 
@@ -594,7 +600,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
       const int slots = is_v ? PC_VSLOTS : PC_KSLOTS, n = s_issued[is_v];
       for (int i = max(0, n - slots); i < n; ++i)
         mbar_drain(is_v ? v_full(i % slots) : k_full(i % slots), (uint32_t)((i / slots) & 1));
-      if (!is_v && s_q_issued > 0) mbar_drain(q_full, (uint32_t)((s_q_issued - 1) & 1));
+      if (is_v && s_q_issued > 0) mbar_drain(q_full, (uint32_t)((s_q_issued - 1) & 1));
     }
   }
   __syncthreads();
