@@ -352,7 +352,7 @@ bitnet_status bitnet_add_rmsnorm_quant_act(const void* x, bitnet_dtype xt, const
  *   slots [T]         its slot (-1 behind the last one)
  * All int32 on the device, 4-byte aligned; n_list is the allocated length of free_pages, n_free
  * [1] how many of its entries are free.  The call takes pages but does not change the list: the
- * caller's new count is n_free_out (which must not be n_free itself).  A calling program returns a
+ * caller's new count is n_free_out.  No output may overlap an input (block_table is both).  A calling program returns a
  * finished request's pages by writing them behind the free ones.
  * If the free pages do not suffice, n_free_out is negative (how many are missing), the entries
  * and slots without a page are -1, and the step must not be run.  A request with a negative
@@ -371,7 +371,8 @@ bitnet_status bitnet_paged_plan(const int32_t* new_lens, const int32_t* ctx_lens
  * its rotated k and its v go to slot slots[t] of the pages.  q_rot is bf16 [T, Hq, 128] here
  * (nearest even; what the paged attention multiplies).  Tokens with a negative slot are skipped:
  * neither their q_rot nor the cache is written.  A slot of n_pages * page_size or more is skipped
- * too and sets BITNET_ERR_INDEX.  The slots of a call must differ from one another.  The angle is
+ * too and sets BITNET_ERR_INDEX.  The slots of a call must differ from one another, and no output
+ * may overlap an input.  The angle is
  * p theta^(-2i/128) reduced to a turn in fp64, its sine and cosine fp32.  Errors: NULL, SHAPE (d != 128, Hq % Hkv,
  * Hq > 1024, page_size, theta <= 0), ALIGN, DTYPE. */
 bitnet_status bitnet_rope_paged_append(const void* q, const void* k, const void* v, bitnet_dtype xt, int64_t T,

@@ -451,6 +451,9 @@ def add_rmsnorm_quant_act(x, residual, gain, eps: float = 1e-6, residual_out=Non
     """x and residual bf16/fp32 [T, K] -> (residual + x in residual's type, q int8 [T, K], s_x fp32 [T],
     sum_q int32 [T]), the last three those of ``rmsnorm_quant_act`` of the first.  ``residual_out`` may be
     ``residual`` itself."""
+    if stream is not None:  # what is allocated here belongs to that stream then
+        with torch.cuda.stream(stream):
+            return add_rmsnorm_quant_act(x, residual, gain, eps, residual_out, out)
     dev = _current(x, "x")
     T, K = x.shape
     n, xt, rt = T * K, _float_code("x", x), _float_code("residual", residual)
@@ -471,7 +474,7 @@ def add_rmsnorm_quant_act(x, residual, gain, eps: float = 1e-6, residual_out=Non
         pq, ps, psq = _arg(dev, "q", q, _I8, n), _arg(dev, "s_x", s, _F32T, T), _arg(dev, "sum_q", sq, _I32, T)
     st = lib().bitnet_add_rmsnorm_quant_act(
         _arg(dev, "x", x, x.dtype, n), xt, _arg(dev, "residual", residual, residual.dtype, n), rt,
-        None if gain is None else _arg(dev, "gain", gain, _F32T, K), eps, T, K, to, pq, ps, psq, _stream(stream))
+        None if gain is None else _arg(dev, "gain", gain, _F32T, K), eps, T, K, to, pq, ps, psq, _stream())
     if st:
         raise BitnetError(st, "add_rmsnorm_quant_act")
     return residual_out, q, s, sq
@@ -480,6 +483,9 @@ def add_rmsnorm_quant_act(x, residual, gain, eps: float = 1e-6, residual_out=Non
 def paged_plan(new_lens, ctx_lens, block_table, free_pages, n_free, page_size: int, T: int, out=None, stream=None):
     """Plan of a step of T tokens (padding included) -> (cu_new [B + 1], kv_lens [B], positions [T], slots [T],
     n_free_out [1]); the requests' new pages are written into ``block_table`` [B, width].  All int32."""
+    if stream is not None:  # what is allocated here belongs to that stream then
+        with torch.cuda.stream(stream):
+            return paged_plan(new_lens, ctx_lens, block_table, free_pages, n_free, page_size, T, out)
     dev = _current(new_lens, "new_lens")
     B, width = block_table.shape
     if T < 0:
@@ -494,13 +500,13 @@ def paged_plan(new_lens, ctx_lens, block_table, free_pages, n_free, page_size: i
     else:
         to = [_arg(dev, nm, t, _I32, n) for nm, t, n in
               zip(("cu_new", "kv_lens", "positions", "slots", "n_free_out"), out, (B + 1, B, T, T, 1), strict=True)]
-        if free_now == to[4]:
-            raise ValueError("n_free_out must not be n_free")
+        if not {free_now, new_lens.data_ptr(), ctx_lens.data_ptr()}.isdisjoint(p for p in to if p):
+            raise ValueError("no output may be an input")
     cu, kv, pos, slots, left = out
     st = lib().bitnet_paged_plan(
         _arg(dev, "new_lens", new_lens, _I32, B), _arg(dev, "ctx_lens", ctx_lens, _I32, B), B, page_size,
         _arg(dev, "block_table", block_table, _I32, B * width), width, _arg(dev, "free_pages", free_pages, _I32, n_list), n_list,
-        free_now, T, *to, _stream(stream))
+        free_now, T, *to, _stream())
     if st:
         raise BitnetError(st, "paged_plan")
     return cu, kv, pos, slots, left
@@ -518,6 +524,9 @@ def rope_paged_append(q, k, v, positions, slots, theta: float, k_pages, v_pages,
     """Rotate q [T, Hq, 128] and k [T, Hkv, 128] (bf16 or fp32) at positions [T]; write k (rotated) and v to slots [T]
     of the bf16 pages [n_pages, Hkv, page_size, 128].  Returns q_rot (bf16 [T, Hq, 128]); tokens with a negative
     slot are skipped."""
+    if stream is not None:  # what is allocated here belongs to that stream then
+        with torch.cuda.stream(stream):
+            return rope_paged_append(q, k, v, positions, slots, theta, k_pages, v_pages, q_rot)
     dev = _current(q, "q")
     T, Hq, d = q.shape
     Hkv, dt, xt = k.shape[1], q.dtype, _float_code("q", q)
@@ -532,7 +541,7 @@ def rope_paged_append(q, k, v, positions, slots, theta: float, k_pages, v_pages,
     st = lib().bitnet_rope_paged_append(
         _arg(dev, "q", q, dt, n), _arg(dev, "k", k, dt, nk), _arg(dev, "v", v, dt, nk), xt, T, Hq, Hkv, d,
         _arg(dev, "positions", positions, _I32, T), _arg(dev, "slots", slots, _I32, T), theta,
-        _arg(dev, "q_rot", q_rot, _BF16T, n), kp, vp, n_pages, P, _stream(stream))
+        _arg(dev, "q_rot", q_rot, _BF16T, n), kp, vp, n_pages, P, _stream())
     if st:
         raise BitnetError(st, "rope_paged_append")
     return q_rot
@@ -547,6 +556,9 @@ def attention_paged(q_rot, k_pages, v_pages, block_table, cu_new, kv_lens, max_n
     """Causal GQA attention of q_rot (bf16 [T, Hq, 128]), the new tokens of B requests back to back (request i:
     rows cu_new[i] .. cu_new[i + 1] - 1, at most max_new), over each request's pages.  Rows of ``out`` behind the
     last request are left as they were."""
+    if stream is not None:  # what is allocated here belongs to that stream then
+        with torch.cuda.stream(stream):
+            return attention_paged(q_rot, k_pages, v_pages, block_table, cu_new, kv_lens, max_new, out_dtype, out, ws)
     dev = _current(q_rot, "q_rot")
     T, Hq, d = q_rot.shape
     B, width = block_table.shape
@@ -568,7 +580,7 @@ def attention_paged(q_rot, k_pages, v_pages, block_table, cu_new, kv_lens, max_n
     st = lib().bitnet_attention_paged(
         _arg(dev, "q_rot", q_rot, _BF16T, n), kp, vp, _arg(dev, "block_table", block_table, _I32, B * width),
         _arg(dev, "cu_new", cu_new, _I32, B + 1), _arg(dev, "kv_lens", kv_lens, _I32, B), T, B, Hq, Hkv, d, n_pages, P, width,
-        max_new, to, _float_code("out", out), _arg(dev, "ws", ws, torch.uint8, nws), nws, _stream(stream))
+        max_new, to, _float_code("out", out), _arg(dev, "ws", ws, torch.uint8, nws), nws, _stream())
     if st:
         raise BitnetError(st, "attention_paged")
     return out

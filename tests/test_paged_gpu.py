@@ -410,6 +410,100 @@ def test_attention_on_other_streams_with_workspaces_of_their_own():
             assert torch.equal(o, a)
 
 
+def test_attention_chunks_captured_and_replayed_on_new_lengths():
+    """A graph of the kernel for many rows, replayed on lengths it was not captured with: one request, ragged ones, none,
+    and a request whose lengths do not fit."""
+    Hq, Hkv, P = 12, 4, 32
+    b = Batch([150, 33, 1, 90], [150, 600, 40, 2000], Hq, Hkv, P, seed=11, pad=5)
+    out = torch.zeros(b.q.shape, dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(tb.attention_paged_workspace_bytes(Hq, Hkv, 280), dtype=torch.uint8, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        tb.attention_paged(b.q, b.kp, b.vp, b.table, b.cu, b.kv, 280, out=out, ws=ws)
+    for new, kv in (([150, 33, 1, 90], [150, 600, 40, 2000]), ([0, 274, 0, 0], [150, 600, 40, 0]), ([1, 1, 1, 1], [2, 599, 33, 1999]),
+                    ([0, 0, 0, 0], [150, 600, 40, 2000]), ([60, 100, 14, 100], [3, 601, 14, 1000])):
+        c = Batch([150, 33, 1, 90], [150, 600, 40, 2000], Hq, Hkv, P, seed=11, pad=5)
+        c.new, c.kvl = new, kv
+        cu = [0]
+        for n in new:
+            cu.append(cu[-1] + n)
+        b.cu.copy_(torch.tensor(cu, dtype=torch.int32))
+        b.kv.copy_(torch.tensor(kv, dtype=torch.int32))
+        c.cu, c.kv = b.cu, b.kv
+        if kv[1] == 601:  # one more row than the request's pages hold: a page id out of range, seen as zeros
+            b.kv[1], c.kvl[1] = b.width * P + 1, 600
+        out.fill_(77.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        bad = kv[1] == 600 and int(b.kv[1]) != 600
+        assert tb.device_status() == (8 if bad else 0)
+        check_attention(c, out, skip=(1,) if bad else ())
+        assert (out[sum(new):] == 77.0).all()
+        if bad:
+            assert (out[60:160] == 77.0).all()
+
+
+@pytest.mark.parametrize("new,kv,Hq,Hkv,P", [([3], [70], 200, 1, 16), ([2, 1], [300, 9], 1024, 4, 32), ([1], [140], 1024, 1, 64),
+                                             ([40], [50], 129, 1, 16)])
+def test_attention_of_more_query_heads_than_a_block(new, kv, Hq, Hkv, P):
+    b = Batch(new, kv, Hq, Hkv, P, seed=Hq)
+    check_attention(b, _attend(b, torch.float32))
+    assert tb.device_status() == 0
+
+
+@pytest.mark.parametrize("new", [1, 130])
+def test_attention_of_pages_that_requests_share(new):
+    """A prefix held once: two requests name the same pages."""
+    b = Batch([new, new], [640, 640], 8, 2, 64, seed=5, nan=False)
+    b.table[1, :8] = b.table[0, :8]
+    check_attention(b, _attend(b, torch.float32), p_round=weight_step(b))
+
+
+def test_attention_on_growing_maxima():
+    """Scores that grow along the cache by more than 2^8 in weight, so that the running maximum moves again and again."""
+    for new in (1, 70):
+        b = Batch([new], [900], 8, 2, 32, seed=6, nan=False)
+        pages = b.table[0, : pages_of(900, 32)].long()
+        ramp = torch.arange(pages.numel() * 32, device=DEV).view(-1, 1, 32, 1) / 8.0
+        b.kp[pages] = (torch.sign(b.q[0, 0]) * ramp / D ** 0.5).bfloat16().expand(-1, 2, -1, -1)
+        b.q = (0.1 * b.q + torch.sign(b.q[0, 0])).bfloat16()
+        check_attention(b, _attend(b, torch.float32), p_round=weight_step(b))
+
+
+def test_attention_wait_limit():
+    """Waits cut to one cycle: the kernel for many rows gives up, says so, and the next call is right."""
+    b = Batch([200, 3], [500, 90], 8, 2, 16, seed=8)
+    try:
+        tb.debug_set_wait_limit(1)
+        tb.attention_paged(b.q, b.kp, b.vp, b.table, b.cu, b.kv, b.max_new)
+        torch.cuda.synchronize()
+        assert tb.device_status() == 7
+    finally:
+        tb.debug_set_wait_limit(0)
+    for _ in range(2):
+        check_attention(b, _attend(b))
+        assert tb.device_status() == 0
+
+
+def test_calls_on_a_given_stream():
+    """Outputs and workspaces that a call allocates belong to the stream it is given."""
+    b = Batch([200, 3], [900, 40], 16, 4, 32, seed=2)
+    x = torch.randn(600, 2560, device=DEV).bfloat16()
+    want, norm = _attend(b), tb.add_rmsnorm_quant_act(x, x, None)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = [tb.attention_paged(b.q, b.kp, b.vp, b.table, b.cu, b.kv, b.max_new, stream=s) for _ in range(4)]
+        got = tb.add_rmsnorm_quant_act(x, x, None, stream=s)
+        junk = [torch.full((1 << 22,), 1.0, device=DEV) for _ in range(4)]  # on the current stream, meanwhile
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o in outs) and all(torch.equal(p, q) for p, q in zip(got, norm))
+        del junk
+
+
 def test_attention_decode_agrees_with_the_contiguous_cache():
     """One request whose pages lie in order is the contiguous cache of attention_decode."""
     T, Hq, Hkv, P, kv = 3, 20, 5, 64, 830
