@@ -376,13 +376,16 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
           const bool bf = a.out_dtype == BITNET_BF16;
           const long long off = r.there ? ((long long)(w.t0 + r.t) * a.Hq + w.head * a.G + r.g) * (bf ? PG_D * 2 : PG_D * 4) : -1;
           const uint32_t stage = sV + PC_VSLOTS * PC_TILE_BYTES + warp * 4096;
+          long long to[8];  // of the rows whose chunk lane & 7 this lane writes
+#pragma unroll
+          for (int i = 0; i < 8; ++i) to[i] = __shfl_sync(0xffffffffu, off, i * 4 + (lane >> 3));
 #pragma unroll 1
           for (int g = 0; g < 4; ++g) {
             float o[32];
             tmem_ld32(tO + 32 * g, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = l == 0.0f ? 0.0f : __fmul_rn(o[k], inv);
+            for (int k = 0; k < 32; ++k) o[k] = __fmul_rn(o[k], inv);
             if (bf) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
@@ -400,8 +403,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
             for (int i = 0; i < 8; ++i) {
               const int rr = i * 4 + (lane >> 3), ch = lane & 7;
               const uint4 x = lds128(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
-              const long long to = __shfl_sync(0xffffffffu, off, rr);
-              if (to >= 0) *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.out) + to + (bf ? (g >> 1) : g) * 128 + ch * 16) = x;
+              if (to[i] >= 0) *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.out) + to[i] + (bf ? (g >> 1) : g) * 128 + ch * 16) = x;
             }
             __syncwarp();
           }
