@@ -1,6 +1,7 @@
 """Python binding of libbitnet_b200.so: the BitNet b1.58 BitLinear forward on B200.
 
-Argument marshalling only -- every step of the arithmetic runs in the library's CUDA
+Argument marshalling only (ctypes; the paged serving step's by the native module
+_serving) -- every step of the arithmetic runs in the library's CUDA
 kernels.  Tensors are torch CUDA tensors (the library allocates no device memory:
 outputs and workspaces are allocated here with torch and passed down); calls are
 enqueued on torch's current stream.  The library must have been built
@@ -409,146 +410,48 @@ def attention_decode(q_rot, k_cache, v_cache, pos0: int, out_dtype=torch.bfloat1
 
 
 # ------------------------------------------------------- a serving step over a paged KV cache
+# These calls are made once per layer and step, often for a few tokens: their checks, allocations and launch
+# are in the native module _serving (csrc/serving_binding.cpp).  With ``stream`` given, what a call allocates
+# belongs to that stream.
 
-# These calls are made once per layer and step, often with a few tokens: their checks are written for
-# a host time of a few microseconds.
-
-_I32, _F32T, _BF16T, _I8 = torch.int32, torch.float32, torch.bfloat16, torch.int8
-
-try:  # the allocation of torch's own generated code: half the time of torch.empty
-    from torch._C._dynamo.guards import _empty_strided_cuda
-except ImportError:
-    def _empty_strided_cuda(size, stride, dtype):
-        return torch.empty(size, dtype=dtype, device="cuda")
+_native = None
 
 
-def _current(t: torch.Tensor, name: str) -> int:
-    """The device of a call's first tensor, which has to be the current one (the stream is its)."""
-    dev = t.get_device()
-    if dev < 0 or dev != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} must be a CUDA tensor on the current device")
-    return dev
-
-
-def _arg(dev: int, name: str, t: torch.Tensor, dtype, numel: int) -> int:
-    """A contiguous tensor's address."""
-    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on cuda:{dev} of type {dtype}")
-    if t.numel() != numel:
-        raise ValueError(f"{name} must have {numel} entries")
-    return t.data_ptr()
-
-
-def _float_code(name: str, t: torch.Tensor) -> int:
-    if t.dtype is _BF16T:
-        return BF16
-    if t.dtype is _F32T:
-        return F32
-    raise ValueError(f"{name} must be of type {_BF16T} or {_F32T}")
+def _load_serving():
+    global _native
+    if _native is None:
+        path = os.path.join(_HERE, "_serving.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it with `python -m ternary_bitlinear_quantized_b200.build`")
+        handle = lib()._handle
+        from . import _serving as native
+        native.bind(handle, BitnetError)
+        _native = native
+    return _native
 
 
 def add_rmsnorm_quant_act(x, residual, gain, eps: float = 1e-6, residual_out=None, out=None, stream=None):
     """x and residual bf16/fp32 [T, K] -> (residual + x in residual's type, q int8 [T, K], s_x fp32 [T],
     sum_q int32 [T]), the last three those of ``rmsnorm_quant_act`` of the first.  ``residual_out`` may be
     ``residual`` itself."""
-    if stream is not None:  # what is allocated here belongs to that stream then
-        with torch.cuda.stream(stream):
-            return add_rmsnorm_quant_act(x, residual, gain, eps, residual_out, out)
-    dev = _current(x, "x")
-    T, K = x.shape
-    n, xt, rt = T * K, _float_code("x", x), _float_code("residual", residual)
-    if residual.shape != x.shape:
-        raise ValueError("residual must have the shape of x")
-    if residual_out is None:
-        residual_out = _empty_strided_cuda((T, K), (K, 1), residual.dtype)
-        to = residual_out.data_ptr()
-    else:
-        if residual_out.shape != x.shape:
-            raise ValueError("residual_out must have the shape of x")
-        to = _arg(dev, "residual_out", residual_out, residual.dtype, n)
-    if out is None:
-        q, s, sq = _empty_strided_cuda((T, K), (K, 1), _I8), _empty_strided_cuda((T,), (1,), _F32T), _empty_strided_cuda((T,), (1,), _I32)
-        pq, ps, psq = q.data_ptr(), s.data_ptr(), sq.data_ptr()
-    else:
-        q, s, sq = out
-        pq, ps, psq = _arg(dev, "q", q, _I8, n), _arg(dev, "s_x", s, _F32T, T), _arg(dev, "sum_q", sq, _I32, T)
-    st = lib().bitnet_add_rmsnorm_quant_act(
-        _arg(dev, "x", x, x.dtype, n), xt, _arg(dev, "residual", residual, residual.dtype, n), rt,
-        None if gain is None else _arg(dev, "gain", gain, _F32T, K), eps, T, K, to, pq, ps, psq, _stream())
-    if st:
-        raise BitnetError(st, "add_rmsnorm_quant_act")
-    return residual_out, q, s, sq
+    return (_native or _load_serving()).add_rmsnorm_quant_act(x, residual, gain, eps, residual_out, out, stream)
 
 
 def paged_plan(new_lens, ctx_lens, block_table, free_pages, n_free, page_size: int, T: int, out=None, stream=None):
     """Plan of a step of T tokens (padding included) -> (cu_new [B + 1], kv_lens [B], positions [T], slots [T],
     n_free_out [1]); the requests' new pages are written into ``block_table`` [B, width].  All int32."""
-    if stream is not None:  # what is allocated here belongs to that stream then
-        with torch.cuda.stream(stream):
-            return paged_plan(new_lens, ctx_lens, block_table, free_pages, n_free, page_size, T, out)
-    dev = _current(new_lens, "new_lens")
-    B, width = block_table.shape
-    if T < 0:
-        raise BitnetError(2, "paged_plan")
-    n_list, free_now = free_pages.numel(), _arg(dev, "n_free", n_free, _I32, 1)
-    if out is None:
-        # one allocation; every part starts on a 4-byte boundary, which is all the step's calls need
-        buf = _empty_strided_cuda((2 * B + 2 + 2 * T,), (1,), _I32)
-        out = buf.split_with_sizes((B + 1, B, T, T, 1))
-        p = buf.data_ptr()
-        to = (p, p + 4 * (B + 1), p + 4 * (2 * B + 1), p + 4 * (2 * B + 1 + T), p + 4 * (2 * B + 1 + 2 * T))
-    else:
-        to = [_arg(dev, nm, t, _I32, n) for nm, t, n in
-              zip(("cu_new", "kv_lens", "positions", "slots", "n_free_out"), out, (B + 1, B, T, T, 1), strict=True)]
-        if not {free_now, new_lens.data_ptr(), ctx_lens.data_ptr()}.isdisjoint(p for p in to if p):
-            raise ValueError("no output may be an input")
-    cu, kv, pos, slots, left = out
-    st = lib().bitnet_paged_plan(
-        _arg(dev, "new_lens", new_lens, _I32, B), _arg(dev, "ctx_lens", ctx_lens, _I32, B), B, page_size,
-        _arg(dev, "block_table", block_table, _I32, B * width), width, _arg(dev, "free_pages", free_pages, _I32, n_list), n_list,
-        free_now, T, *to, _stream())
-    if st:
-        raise BitnetError(st, "paged_plan")
-    return cu, kv, pos, slots, left
-
-
-def _pages(dev: int, k_pages, v_pages, Hkv: int, d: int):
-    shape = k_pages.shape
-    if len(shape) != 4 or shape != v_pages.shape or shape[3] != d or shape[1] != Hkv:
-        raise ValueError("k_pages and v_pages must be [n_pages, Hkv, page_size, d]")
-    n = k_pages.numel()
-    return shape[0], shape[2], _arg(dev, "k_pages", k_pages, _BF16T, n), _arg(dev, "v_pages", v_pages, _BF16T, n)
+    return (_native or _load_serving()).paged_plan(new_lens, ctx_lens, block_table, free_pages, n_free, page_size, T, out, stream)
 
 
 def rope_paged_append(q, k, v, positions, slots, theta: float, k_pages, v_pages, q_rot=None, stream=None) -> torch.Tensor:
     """Rotate q [T, Hq, 128] and k [T, Hkv, 128] (bf16 or fp32) at positions [T]; write k (rotated) and v to slots [T]
     of the bf16 pages [n_pages, Hkv, page_size, 128].  Returns q_rot (bf16 [T, Hq, 128]); tokens with a negative
     slot are skipped."""
-    if stream is not None:  # what is allocated here belongs to that stream then
-        with torch.cuda.stream(stream):
-            return rope_paged_append(q, k, v, positions, slots, theta, k_pages, v_pages, q_rot)
-    dev = _current(q, "q")
-    T, Hq, d = q.shape
-    Hkv, dt, xt = k.shape[1], q.dtype, _float_code("q", q)
-    if k.shape != (T, Hkv, d) or v.shape != k.shape:
-        raise ValueError("k and v must be [T, Hkv, d]")
-    n_pages, P, kp, vp = _pages(dev, k_pages, v_pages, Hkv, d)
-    if q_rot is None:
-        q_rot = _empty_strided_cuda((T, Hq, d), (Hq * d, d, 1), _BF16T)
-    elif q_rot.shape != q.shape:
-        raise ValueError("q_rot must have the shape of q")
-    n, nk = T * Hq * d, T * Hkv * d
-    st = lib().bitnet_rope_paged_append(
-        _arg(dev, "q", q, dt, n), _arg(dev, "k", k, dt, nk), _arg(dev, "v", v, dt, nk), xt, T, Hq, Hkv, d,
-        _arg(dev, "positions", positions, _I32, T), _arg(dev, "slots", slots, _I32, T), theta,
-        _arg(dev, "q_rot", q_rot, _BF16T, n), kp, vp, n_pages, P, _stream())
-    if st:
-        raise BitnetError(st, "rope_paged_append")
-    return q_rot
+    return (_native or _load_serving()).rope_paged_append(q, k, v, positions, slots, theta, k_pages, v_pages, q_rot, stream)
 
 
 def attention_paged_workspace_bytes(Hq: int, Hkv: int, max_new: int) -> int:
-    return lib().bitnet_attention_paged_workspace_bytes(Hq, Hkv, max_new)
+    return int(lib().bitnet_attention_paged_workspace_bytes(Hq, Hkv, max_new))
 
 
 def attention_paged(q_rot, k_pages, v_pages, block_table, cu_new, kv_lens, max_new: int, out_dtype=torch.bfloat16,
@@ -556,34 +459,8 @@ def attention_paged(q_rot, k_pages, v_pages, block_table, cu_new, kv_lens, max_n
     """Causal GQA attention of q_rot (bf16 [T, Hq, 128]), the new tokens of B requests back to back (request i:
     rows cu_new[i] .. cu_new[i + 1] - 1, at most max_new), over each request's pages.  Rows of ``out`` behind the
     last request are left as they were."""
-    if stream is not None:  # what is allocated here belongs to that stream then
-        with torch.cuda.stream(stream):
-            return attention_paged(q_rot, k_pages, v_pages, block_table, cu_new, kv_lens, max_new, out_dtype, out, ws)
-    dev = _current(q_rot, "q_rot")
-    T, Hq, d = q_rot.shape
-    B, width = block_table.shape
-    Hkv = k_pages.shape[1]
-    n_pages, P, kp, vp = _pages(dev, k_pages, v_pages, Hkv, d)
-    n = T * Hq * d
-    if out is None:
-        out = _empty_strided_cuda((T, Hq, d), (Hq * d, d, 1), out_dtype)
-        to = out.data_ptr()
-    else:
-        if out.shape != q_rot.shape:
-            raise ValueError("out must have the shape of q_rot")
-        to = _arg(dev, "out", out, out.dtype, n)
-    if ws is None:
-        nws = max(lib().bitnet_attention_paged_workspace_bytes(Hq, Hkv, max_new), 16)
-        ws = _empty_strided_cuda((nws,), (1,), torch.uint8)
-    else:
-        nws = ws.numel()
-    st = lib().bitnet_attention_paged(
-        _arg(dev, "q_rot", q_rot, _BF16T, n), kp, vp, _arg(dev, "block_table", block_table, _I32, B * width),
-        _arg(dev, "cu_new", cu_new, _I32, B + 1), _arg(dev, "kv_lens", kv_lens, _I32, B), T, B, Hq, Hkv, d, n_pages, P, width,
-        max_new, to, _float_code("out", out), _arg(dev, "ws", ws, torch.uint8, nws), nws, _stream())
-    if st:
-        raise BitnetError(st, "attention_paged")
-    return out
+    return (_native or _load_serving()).attention_paged(q_rot, k_pages, v_pages, block_table, cu_new, kv_lens, max_new, out_dtype,
+                                                   out, ws, stream)
 
 
 def debug_set_wait_limit(cycles: int) -> None:

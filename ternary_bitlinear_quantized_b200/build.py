@@ -1,4 +1,4 @@
-"""Build libbitnet_b200.so in-tree with nvcc for sm_100a (B200).
+"""Build libbitnet_b200.so (nvcc, sm_100a) and the native part of its Python binding (g++) in-tree.
 
 Usage: ``python -m ternary_bitlinear_quantized_b200.build [--verbose]``.  nvcc
 cross-compiles without a GPU.  The library links the CUDA runtime statically, so it
@@ -14,6 +14,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libbitnet_b200.so")
+BINDING = os.path.join(HERE, "_serving.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -29,24 +30,43 @@ def sources() -> list[str]:
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
-    srcs = sources()
     hdr = os.path.join(os.path.dirname(HERE), "include", "bitnet_b200.h")
-    newest = max(os.path.getmtime(p) for p in srcs + [hdr, __file__])
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:
-        return LIB
-    cmd = [nvcc(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "--fmad=false", "-Xcompiler", "-fPIC", "-shared",
-           "-cudart", "static", "-I", os.path.join(os.path.dirname(HERE), "include"),
-           "-o", LIB + ".tmp", os.path.join(CSRC, "bitnet_b200.cu")]
+    include = ["-I", os.path.dirname(hdr)]
+    _run(LIB, sources() + [hdr], [nvcc(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "--fmad=false", "-Xcompiler", "-fPIC",
+                                  "-shared", "-cudart", "static", *include, os.path.join(CSRC, "bitnet_b200.cu"),
+                                  *(["-Xptxas=-v"] if verbose else [])], verbose, force)
+    src = os.path.join(CSRC, "serving_binding.cpp")
+    if force or _stale(BINDING, [src, hdr]):  # the import of torch takes longer than the check
+        import sysconfig
+
+        import torch
+        root = os.path.dirname(torch.__file__)
+        cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+        dirs = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], cuda]
+        _run(BINDING, [src, hdr], [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+                                   f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                                   *[f"-I{d}" for d in dirs], src, "-L" + os.path.join(root, "lib"), "-ltorch_python",
+                                   "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-ltorch"], verbose, force)
+    return LIB
+
+
+def _stale(out: str, srcs: list[str]) -> bool:
+    return not os.path.exists(out) or os.path.getmtime(out) < max(os.path.getmtime(p) for p in srcs + [__file__])
+
+
+def _run(out: str, srcs: list[str], cmd: list[str], verbose: bool, force: bool) -> None:
+    if not force and not _stale(out, srcs):
+        return
+    cmd = cmd + ["-o", out + ".tmp"]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
     if verbose:
         print(res.stderr, file=sys.stderr)
-    os.replace(LIB + ".tmp", LIB)
-    return LIB
+    os.replace(out + ".tmp", out)
 
 
 if __name__ == "__main__":
