@@ -380,30 +380,31 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
 #pragma unroll
           for (int i = 0; i < 8; ++i) to[i] = __shfl_sync(0xffffffffu, off, i * 4 + (lane >> 3));
 #pragma unroll 1
-          for (int g = 0; g < 4; ++g) {
-            float o[32];
-            tmem_ld32(tO + 32 * g, o);
+          for (int g = 0; g < 8; ++g) {
+            float o[16];
+            tmem_ld16f(tO + 16 * g, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __fmul_rn(o[k], inv);
+            for (int k = 0; k < 16; ++k) o[k] = __fmul_rn(o[k], inv);
             if (bf) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                sts128(stage + lane * 128 + ((((g & 1) * 4 + k) ^ (lane & 7)) << 4), pack_bf16(o[8 * k], o[8 * k + 1]),
+              for (int k = 0; k < 2; ++k)
+                sts128(stage + lane * 128 + ((((g & 3) * 2 + k) ^ (lane & 7)) << 4), pack_bf16(o[8 * k], o[8 * k + 1]),
                        pack_bf16(o[8 * k + 2], o[8 * k + 3]), pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
-              if ((g & 1) == 0) continue;
+              if ((g & 3) != 3) continue;
             } else {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                sts128(stage + lane * 128 + ((k ^ (lane & 7)) << 4), __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
+              for (int k = 0; k < 4; ++k)
+                sts128(stage + lane * 128 + ((((g & 1) * 4 + k) ^ (lane & 7)) << 4), __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
                        __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
+              if ((g & 1) == 0) continue;
             }
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int rr = i * 4 + (lane >> 3), ch = lane & 7;
               const uint4 x = lds128(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
-              if (to[i] >= 0) *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.out) + to[i] + (bf ? (g >> 1) : g) * 128 + ch * 16) = x;
+              if (to[i] >= 0) *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.out) + to[i] + (bf ? g >> 2 : g >> 1) * 128 + ch * 16) = x;
             }
             __syncwarp();
           }
@@ -443,60 +444,57 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
           if (rows) umma_commit(bar);
           else mbar_arrive(bar);
         };
-        auto next_k = [&]() {
-          release(k_empty(ks));
-          if (++ks == PC_KSLOTS) {
-            ks = 0;
-            ph_k ^= 1u;
-          }
-        };
-        ok = mbar_wait_bounded(q_full, ph_q) && mbar_wait_bounded(k_full(ks), ph_k);
-        if (!ok) break;
-        ph_q ^= 1u;
-        tc_fence_after();
-        if (rows) {
-          const uint32_t k = (sK + ks * PC_TILE_BYTES) >> 4 | PC_DESC_K;
-          pc_scores<0>(h, q, k);
-          umma_commit(s_full(h, 0));
-          pc_scores<1>(h, q, k);
-          umma_commit(s_full(h, 1));
-        }
-        next_k();
-        if (cnt == 1) release(q_empty);
-        for (int it = 0; it < cnt; ++it) {
-          const bool more = it + 1 < cnt;
-          ok = mbar_wait_bounded(v_full(vs), ph_v);
-          if (ok && pc_tail(a, w.kv, w.unit + it) > 0) {
-            ok = mbar_wait_bounded(v_fixed(vs), (ph_f >> vs) & 1u);
-            ph_f ^= 1u << vs;
+        // One loop for the first scores (it = -1) and the rest: what runs once per tile would have left
+        // the instruction cache, which costs about 1000 cycles a miss.
+        for (int it = -1; it < cnt; ++it) {
+          const bool have = it >= 0, more = it + 1 < cnt;
+          if (have) {
+            ok = mbar_wait_bounded(v_full(vs), ph_v);
+            if (ok && pc_tail(a, w.kv, w.unit + it) > 0) {
+              ok = mbar_wait_bounded(v_fixed(vs), (ph_f >> vs) & 1u);
+              ph_f ^= 1u << vs;
+            }
+          } else {
+            ok = mbar_wait_bounded(q_full, ph_q);
+            ph_q ^= 1u;
           }
           if (more) ok = ok && mbar_wait_bounded(k_full(ks), ph_k);
           if (!ok) break;
           if (rows) {
             const uint32_t v = (sV + vs * PC_TILE_BYTES) >> 4 | PC_DESC_V, k = (sK + ks * PC_TILE_BYTES) >> 4 | PC_DESC_K;
-            ok = mbar_wait_bounded(p_full(h, 0), ph_p);
+            if (have) ok = mbar_wait_bounded(p_full(h, 0), ph_p);
             if (!ok) break;
             tc_fence_after();
-            pc_values<0>(h, v, it == 0);
+            if (have) pc_values<0>(h, v, it == 0);
             if (more) pc_scores<0>(h, q, k);
             umma_commit(s_full(h, 0));
-            ok = mbar_wait_bounded(p_full(h, 1), ph_p);
-            if (!ok) break;
-            ph_p ^= 1u;
-            tc_fence_after();
-            pc_values<1>(h, v, false);
+            if (have) {
+              ok = mbar_wait_bounded(p_full(h, 1), ph_p);
+              if (!ok) break;
+              ph_p ^= 1u;
+              tc_fence_after();
+              pc_values<1>(h, v, false);
+            }
             if (more) pc_scores<1>(h, q, k);
           }
-          if (more) next_k();
-          if (it + 2 == cnt) release(q_empty);
-          release(v_empty(vs));
-          if (rows) umma_commit(s_full(h, 1));
-          if (++vs == PC_VSLOTS) {
-            vs = 0;
-            ph_v ^= 1u;
+          if (more) {
+            release(k_empty(ks));
+            if (++ks == PC_KSLOTS) {
+              ks = 0;
+              ph_k ^= 1u;
+            }
           }
+          if (it + 2 == cnt) release(q_empty);
+          if (have) {
+            release(v_empty(vs));
+            if (++vs == PC_VSLOTS) {
+              vs = 0;
+              ph_v ^= 1u;
+            }
+          }
+          if (rows) umma_commit(s_full(h, 1));
         }
-        }
+      }
       if (!ok) s_abort = 1;
       umma_commit(mma_done);  // every product ends before tensor memory is released, also after an abort
       mbar_drain(mma_done, 0);
