@@ -85,8 +85,8 @@ BN_DEV int tile_units(const PagedArgs& a, int n, int kv, int j) {
 
 // A CTA's place on the line of units.
 struct PagedWalkShared {
-  long long warp_sum[32], pr0, pr1;
-  int seq, t0, n, kv, tile, at;
+  long long warp_sum[32];
+  int seq, t0, n, kv, head, tile, at;
 };
 template <typename Tiles>
 struct PagedWalk {
@@ -129,13 +129,13 @@ struct PagedWalk {
   // The descriptor of this tile, which began in another CTA's share.
   BN_DEV PagedTile ended() const { return {(int)div_nonneg(pos - at + Tiles::FIXED, per), t0, n, head, tile}; }
 
-  // Block-wide: finds the CTA's share.  Up to blockDim requests are taken at once, S threads (a
-  // power of two) per request, each with q consecutive tiles of one head; prefix sums over the
-  // threads give the place of each request (times Hkv) and of each thread's tiles in a head.
+  // Block-wide: finds the CTA's share.  Up to blockDim requests are taken at once, S threads of one
+  // warp (a power of two) per request, each with q consecutive tiles of one head; prefix sums over
+  // the threads give the place of each request (times Hkv) and of each thread's tiles in a head.
   BN_DEV void begin(const PagedArgs& a, int C, PagedWalkShared* sm) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     int logS = 0;
-    while ((a.B << (logS + 1)) <= (int)blockDim.x) ++logS;
+    while (logS < 5 && (a.B << (logS + 1)) <= (int)blockDim.x) ++logS;
     const int S = 1 << logS, sub = threadIdx.x & (S - 1), per_round = blockDim.x >> logS;
     bool bad = false;
     int rt0, rn, rkv, j0, j1;  // this thread's request and tiles of the last round
@@ -161,7 +161,6 @@ struct PagedWalk {
         const long long x = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += x;
       }
-      __syncthreads();  // the sums of the round before have been read
       if (lane == 31) sm->warp_sum[warp] = v;
       __syncthreads();
       all = 0;
@@ -172,10 +171,10 @@ struct PagedWalk {
       }
       return v;
     };
-    if (threadIdx.x == 0) sm->seq = 0x7FFFFFFF;
     long long total = 0, incl = 0, mine = 0, last_round = 0;
     const int rounds = (a.B + per_round - 1) / per_round;
     for (int r = 0; r < rounds; ++r) {
+      if (r > 0) __syncthreads();  // the sums of the round before have been read
       mine = mine_of(r * per_round + (threadIdx.x >> logS));
       incl = total + scan(mine, last_round);
       total += last_round;
@@ -190,47 +189,43 @@ struct PagedWalk {
     int round = rounds - 1;
     while (pos < before * a.Hkv) {  // from the last round, whose sums are at hand, downwards
       --round;
+      __syncthreads();
       mine = mine_of(round * per_round + (threadIdx.x >> logS));
       long long all;
       incl = scan(mine, all);
       before -= all;
       incl += before;
     }
-    // the request: the first whose end lies behind pos (this round's are consecutive)
+    // the threads of the request that pos lies in, and of them the one whose tiles it lies in
     const long long start = incl - mine;
-    __syncthreads();  // the last round's sums have been read, seq is set
-    if (sub == S - 1 && pos < incl * a.Hkv) atomicMin(&sm->seq, (int)(threadIdx.x >> logS));
-    __syncthreads();
-    const bool in_request = (int)(threadIdx.x >> logS) == sm->seq;
-    if (in_request && sub == 0) {
-      sm->pr0 = start;
-      sm->t0 = rt0;
-      sm->n = rn;
-      sm->kv = rkv;
-    }
-    if (in_request && sub == S - 1) sm->pr1 = incl;
-    __syncthreads();
-    const long long w = sm->pr1 - sm->pr0, off = pos - sm->pr0 * a.Hkv;
-    head = (int)div_nonneg(off, w);
-    const long long target = sm->pr0 + (off - head * w);
-    if (in_request && target >= start && target < incl) {
-      long long rem = target - start;
-      int j = j0;
-      for (;; ++j) {
-        const int u = tile_units<Tiles>(a, rn, rkv, j) + Tiles::FIXED;
-        if (rem < u) break;
-        rem -= u;
+    const long long pr0 = __shfl_sync(0xffffffffu, start, lane & ~(S - 1)), pr1 = __shfl_sync(0xffffffffu, incl, lane | (S - 1));
+    if (pr0 * a.Hkv <= pos && pos < pr1 * a.Hkv) {
+      const long long w = pr1 - pr0, off = pos - pr0 * a.Hkv, hd = div_nonneg(off, w), target = pr0 + off - hd * w;
+      if (target >= start && target < incl) {
+        long long rem = target - start;
+        int j = j0;
+        for (;; ++j) {
+          const int u = tile_units<Tiles>(a, rn, rkv, j) + Tiles::FIXED;
+          if (rem < u) break;
+          rem -= u;
+        }
+        sm->seq = round * per_round + (threadIdx.x >> logS);
+        sm->t0 = rt0;
+        sm->n = rn;
+        sm->kv = rkv;
+        sm->head = (int)hd;
+        sm->tile = j;
+        sm->at = (int)rem;
       }
-      sm->tile = j;
-      sm->at = (int)rem;
     }
     __syncthreads();
+    seq = sm->seq;
     t0 = sm->t0;
     n = sm->n;
     kv = sm->kv;
+    head = sm->head;
     tile = sm->tile;
     at = sm->at;
-    seq = round * per_round + sm->seq;
     blocks = Tiles::blocks(a, n);
     nu = tile_units<Tiles>(a, n, kv, tile);
   }
@@ -443,71 +438,73 @@ __global__ void __launch_bounds__(PD_THREADS, 2) k_attn_paged_few(const PagedArg
       l[e] = __fadd_rn(l[e], __shfl_xor_sync(0xffffffffu, l[e], 1));
       l[e] = __fadd_rn(l[e], __shfl_xor_sync(0xffffffffu, l[e], 2));
     }
-    // join the four warps: 1 into 0 and 3 into 2, then 2 into 0, through the giver's ring (drained)
+    // Join the four warps: each leaves its values in its ring (drained), then each adds up a quarter of
+    // the columns, blocks 4 warp .. 4 warp + 3 of eight.
+    {
+      float* buf = reinterpret_cast<float*>(pd_sm + warp * PD_STAGES * PD_STAGE_BYTES) + lane;
 #pragma unroll
-    for (int step = 1; step <= 2; ++step) {
-      const bool gives = (warp & (2 * step - 1)) == step, takes = (warp & (2 * step - 1)) == 0;
-      float* buf = reinterpret_cast<float*>(pd_sm + (warp | step) * PD_STAGES * PD_STAGE_BYTES) + lane;
-      if (gives) {
+      for (int i = 0; i < 64; ++i) buf[i * 32] = O[i >> 2][i & 3];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) buf[i * 32] = O[i >> 2][i & 3];
-        buf[64 * 32] = m[0];
-        buf[65 * 32] = m[1];
-        buf[66 * 32] = l[0];
-        buf[67 * 32] = l[1];
+      for (int e = 0; e < 2; ++e) {
+        buf[(64 + e) * 32] = m[e];
+        buf[(66 + e) * 32] = l[e];
       }
-      __syncthreads();
-      if (takes) {
-        float f[2], h[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float mo = buf[(64 + e) * 32], mn = fmaxf(m[e], mo);
-          const float mu = mn == -INFINITY ? 0.0f : mn;
-          f[e] = exp2_approx(__fsub_rn(m[e], mu));
-          h[e] = exp2_approx(__fsub_rn(mo, mu));
-          m[e] = mn;
-          l[e] = __fmaf_rn(l[e], f[e], __fmul_rn(buf[(66 + e) * 32], h[e]));
-        }
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          const int e = (i >> 1) & 1;
-          O[i >> 2][i & 3] = __fmaf_rn(O[i >> 2][i & 3], f[e], __fmul_rn(buf[i * 32], h[e]));
-        }
-      }
-      __syncthreads();  // the ring is filled again for the next tile
     }
-    if (warp == 0) {
-      if (cnt == nu) {
+    __syncthreads();
+    float o[16];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (qoff[e] < 0) continue;
-          const float inv = l[e] > 0.0f ? __fdiv_rn(1.0f, l[e]) : (l[e] == 0.0f ? 0.0f : l[e]);  // NaN stays
+    for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+    {
+      const float* buf = reinterpret_cast<const float*>(pd_sm) + lane;
+      constexpr int STRIDE = PD_STAGES * PD_STAGE_BYTES / 4;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float x = __fmul_rn(O[i][2 * e], inv), y = __fmul_rn(O[i][2 * e + 1], inv);
-            const long long off = qoff[e] + i * 8 + 2 * tq;
-            if (a.out_dtype == BITNET_BF16)
-              *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) + off) = pack_bf16(x, y);
-            else
-              *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + off) = make_float2(x, y);
-          }
-        }
-      } else {
-        float* part = a.part + ((long long)blockIdx.x * 2 + (w.unit > 0 ? 0 : 1)) * PD_PART;
+      for (int e = 0; e < 2; ++e) {
+        float mv[PD_WARPS];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int v = 0; v < PD_WARPS; ++v) mv[v] = buf[v * STRIDE + (64 + e) * 32];
+        m[e] = fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3]));
+        const float mu = m[e] == -INFINITY ? 0.0f : m[e];
+        l[e] = 0.0f;
+#pragma unroll
+        for (int v = 0; v < PD_WARPS; ++v) {
+          const float f = exp2_approx(__fsub_rn(mv[v], mu));
+          l[e] = __fmaf_rn(buf[v * STRIDE + (66 + e) * 32], f, l[e]);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            *reinterpret_cast<float2*>(part + (g + 8 * e) * PG_D + i * 8 + 2 * tq) = make_float2(O[i][2 * e], O[i][2 * e + 1]);
-          if (tq == 0) {
-            part[PD_M * PG_D + g + 8 * e] = m[e];
-            part[PD_M * PG_D + PD_M + g + 8 * e] = l[e];
-          }
+            if (((i >> 1) & 1) == e) o[i] = __fmaf_rn(buf[v * STRIDE + (16 * warp + i) * 32], f, o[i]);
         }
-        if (lane == 0 && w.unit > 0 && w.unit + cnt == nu)
-          a.desc[blockIdx.x] = w.ended();
       }
     }
+    if (cnt == nu) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (qoff[e] < 0) continue;
+        const float inv = l[e] > 0.0f ? __fdiv_rn(1.0f, l[e]) : (l[e] == 0.0f ? 0.0f : l[e]);  // NaN stays
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = __fmul_rn(o[4 * i + 2 * e], inv), y = __fmul_rn(o[4 * i + 2 * e + 1], inv);
+          const long long off = qoff[e] + (4 * warp + i) * 8 + 2 * tq;
+          if (a.out_dtype == BITNET_BF16)
+            *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) + off) = pack_bf16(x, y);
+          else
+            *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + off) = make_float2(x, y);
+        }
+      }
+    } else {
+      float* part = a.part + ((long long)blockIdx.x * 2 + (w.unit > 0 ? 0 : 1)) * PD_PART;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float2*>(part + (g + 8 * e) * PG_D + (4 * warp + i) * 8 + 2 * tq) = make_float2(o[4 * i + 2 * e], o[4 * i + 2 * e + 1]);
+        if (tq == 0 && warp == 0) {
+          part[PD_M * PG_D + g + 8 * e] = m[e];
+          part[PD_M * PG_D + PD_M + g + 8 * e] = l[e];
+        }
+      }
+      if (threadIdx.x == 0 && w.unit > 0 && w.unit + cnt == nu) a.desc[blockIdx.x] = w.ended();
+    }
+    __syncthreads();  // the rings are filled again for the next tile
   }
 }
 
