@@ -1286,7 +1286,7 @@ bitnet_status bitnet_paged_plan(const int32_t* new_lens, const int32_t* ctx_lens
   const long long ctas = (T + PLAN_TOKENS - 1) / PLAN_TOKENS;
   const cudaError_t e = launch(k_paged_plan, dim3((unsigned)(ctas > 0 ? ctas : 1)), dim3(PLAN_THREADS),
                                (size_t)(B + 1) * 8, reinterpret_cast<cudaStream_t>(stream), true, new_lens, ctx_lens,
-                               (int)B, (int)page_size, block_table, (int)width, free_pages, (int)n_list, n_free, (int)T,
+                               (int)B, page_log2(page_size), block_table, (int)width, free_pages, (int)n_list, n_free, (int)T,
                                cu_new, kv_lens, positions, slots, n_free_out);
   return e == cudaSuccess ? BITNET_OK : cuda_fail(e, "k_paged_plan");
 }

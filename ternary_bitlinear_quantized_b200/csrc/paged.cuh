@@ -18,26 +18,30 @@ constexpr int PG_MAX_REQUESTS = 4096;   // k_paged_plan keeps two prefix sums of
 
 BN_DEV void flag_index_error() { atomicExch(&g_device_status, (int)BITNET_ERR_INDEX); }
 
-// Inclusive prefix sum over the block of one int per thread; `total` is the block's sum.
-// `scratch`: 32 ints of shared memory; ends with a barrier that protects it.
-BN_DEV int block_scan_incl(int v, int* scratch, int& total) {
+// Inclusive prefix sums over the block of two numbers per thread, and the block's sums.
+// `scratch`: 64 long longs of shared memory, not read or written otherwise.
+BN_DEV void block_scan_incl2(long long (&v)[2], long long* scratch, long long (&total)[2]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  if (lane == 31) scratch[warp] = v;
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < nw; ++w) {
-    const int s = scratch[w];
-    if (w < warp) before += s;
-    all += s;
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const long long u = __shfl_up_sync(0xffffffffu, v[k], o);
+      if (lane >= o) v[k] += u;
+    }
+  if (lane == 31) {
+    scratch[2 * warp] = v[0];
+    scratch[2 * warp + 1] = v[1];
   }
   __syncthreads();
-  total = all;
-  return v + before;
+  total[0] = total[1] = 0;
+  for (int w = 0; w < nw; ++w)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const long long s = scratch[2 * w + k];
+      if (w < warp) v[k] += s;
+      total[k] += s;
+    }
 }
 
 // Largest i in [0, n) with a[i] <= x, for ascending a with a[0] <= x.
@@ -63,19 +67,20 @@ BN_DEV int last_not_above(const int* a, int n, int x) {
 // page is read from the free list directly, not from the table entry that another CTA may be
 // writing.
 constexpr int PLAN_THREADS = 256;
-constexpr int PLAN_TOKENS = 1024;  // tokens per CTA
+constexpr int PLAN_TOKENS = 256;  // tokens per CTA: 36371 tokens of 96 requests 3.9 us, with 1024 per CTA 6.4 us
 __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const int* __restrict__ new_lens, const int* __restrict__ ctx_lens,
-                                                             int B, int P, int* table, int width,
+                                                             int B, int log2P, int* table, int width,
                                                              const int* __restrict__ free_pages, int n_list,
                                                              const int* __restrict__ n_free, int T, int* __restrict__ cu_out,
                                                              int* __restrict__ kv_out, int* __restrict__ pos_out,
                                                              int* __restrict__ slot_out, int* __restrict__ n_free_out) {
   extern __shared__ int plan_sm[];
-  __shared__ int scratch[32];
+  __shared__ long long scratch[64];
   int* cu = plan_sm;            // [B + 1] tokens before request i
   int* start = plan_sm + B + 1; // [B + 1] new pages before request i
   pdl_launch_dependents();
   pdl_wait();
+  const int P = 1 << log2P;
   const long long cap = (long long)width * P;
   bool bad = false;
   int nf = __ldg(n_free);
@@ -85,9 +90,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const int* __restri
   }
   // A request's lengths; one that does not fit its row of the table keeps its place among the
   // tokens, but gets no pages and no slots.
-  auto read = [&](int i, int& n, int& c, bool& fits) {
-    n = __ldg(new_lens + i);
-    c = __ldg(ctx_lens + i);
+  auto judge = [&](int& n, int& c, bool& fits) {
     fits = true;
     if (n < 0 || c < 0 || c + (long long)n > cap) {
       bad = true;
@@ -102,34 +105,44 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const int* __restri
   };
   // slot of row r of a page; ids below 0 stand for no page, others must keep the slot an int32
   auto slot_of = [&](int page, int r) {
-    if (page > (0x7FFFFFFF - r) / P) {
+    if (page > (0x7FFFFFFF - r) >> log2P) {
       bad = true;
       return -1;
     }
-    return page < 0 ? -1 : page * P + r;
+    return page < 0 ? -1 : (page << log2P) + r;
   };
-  long long tok = 0, pg = 0;
-  for (int i0 = 0; i0 < B; i0 += PLAN_THREADS) {
-    const int i = i0 + threadIdx.x;
-    int n = 0, need = 0;
-    if (i < B) {
-      int c;
-      bool fits;
-      read(i, n, c, fits);
-      if (fits) need = (c + n + P - 1) / P - (c + P - 1) / P;
-      if (blockIdx.x == 0) kv_out[i] = fits ? c + n : c;
-    }
-    // 32-bit block sums hold: n <= T <= 2^22, need <= n / 16 + 1
-    int tn, tp;
-    const int sn = block_scan_incl(n, scratch, tn), sp = block_scan_incl(need, scratch, tp);
-    if (i < B) {
-      const long long a = tok + sn - n;
-      cu[i] = (int)min(a, (long long)T);
-      start[i] = (int)(pg + sp - need);
-    }
-    tok += tn;
-    pg += tp;
+  // q consecutive requests a thread
+  const int q = (B + PLAN_THREADS - 1) / PLAN_THREADS, i0 = min(B, (int)threadIdx.x * q), i1 = min(B, i0 + q);
+  auto pages = [&](int n, int c, bool fits) { return fits ? ((c + n + P - 1) >> log2P) - ((c + P - 1) >> log2P) : 0; };
+  for (int i = threadIdx.x; i < B; i += PLAN_THREADS) {  // the lengths, in the places of the sums
+    cu[i] = __ldg(new_lens + i);
+    start[i] = __ldg(ctx_lens + i);
   }
+  __syncthreads();
+  long long sum[2] = {0, 0}, total[2];  // tokens, new pages
+  for (int i = i0; i < i1; ++i) {
+    int n = cu[i], c = start[i];
+    bool fits;
+    judge(n, c, fits);
+    sum[0] += n;
+    sum[1] += pages(n, c, fits);
+  }
+  long long at0 = sum[0], at1 = sum[1];
+  block_scan_incl2(sum, scratch, total);
+  at0 = sum[0] - at0;
+  at1 = sum[1] - at1;
+  for (int i = i0; i < i1; ++i) {
+    int n = cu[i], c = start[i];
+    bool fits;
+    judge(n, c, fits);
+    cu[i] = (int)min(at0, (long long)T);
+    start[i] = (int)at1;
+    if (blockIdx.x == 0) kv_out[i] = fits ? c + n : c;
+    at0 += n;
+    at1 += pages(n, c, fits);
+  }
+  long long tok = total[0];
+  const long long pg = total[1];  // at most (T / 16 + 1) B < 2^31
   if (tok > T) {
     bad = true;
     tok = T;
@@ -148,7 +161,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const int* __restri
     const int i = last_not_above(start, B, e);
     const int c = __ldg(ctx_lens + i);
     const int at = nf - 1 - e;
-    table[(long long)i * width + (c + P - 1) / P + (e - start[i])] = at >= 0 ? __ldg(free_pages + at) : -1;
+    table[(long long)i * width + ((c + P - 1) >> log2P) + (e - start[i])] = at >= 0 ? __ldg(free_pages + at) : -1;
   }
   // tokens
   const int t1 = min(T, (int)(blockIdx.x + 1) * PLAN_TOKENS);
@@ -156,12 +169,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const int* __restri
     int pos = 0, slot = -1;
     if (t < (int)tok) {
       const int i = last_not_above(cu, B, t);
-      int n, c;
+      int n = __ldg(new_lens + i), c = __ldg(ctx_lens + i);
       bool fits;
-      read(i, n, c, fits);
+      judge(n, c, fits);
       pos = c + t - cu[i];
       if (fits) {
-        const int pi = pos / P, old = (c + P - 1) / P;
+        const int pi = pos >> log2P, old = (c + P - 1) >> log2P;
         int page;
         if (pi < old) {
           page = table[(long long)i * width + pi];
@@ -169,7 +182,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const int* __restri
           const int at = nf - 1 - start[i] - (pi - old);
           page = at >= 0 ? __ldg(free_pages + at) : -1;
         }
-        slot = slot_of(page, pos % P);
+        slot = slot_of(page, pos & (P - 1));
       }
     }
     pos_out[t] = pos;
