@@ -1,7 +1,7 @@
 // The Python side of a serving step's calls (add_rmsnorm_quant_act, paged_plan, rope_paged_append,
 // attention_paged): argument checks, outputs and workspaces from torch's allocator, the current
 // stream.  They are made once per layer and step, most often for a few tokens, where the GPU
-// takes 3-10 us: in Python over ctypes a call took 11-14 us of host time, here 6-8, 3 of them the launch.
+// takes 3-10 us: in Python over ctypes a call took 11-14 us of host time, here 5-7, 2-3 of them the launch.
 // The library itself stays the plain C one: its entry points are looked up in the handle that the
 // package loaded.
 #include <ATen/cuda/EmptyTensor.h>
@@ -76,6 +76,14 @@ at::Tensor make(int dev, at::IntArrayRef size, at::ScalarType type) {
   return at::Tensor(at::detail::empty_cuda(size, type, at::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt));
 }
 
+// `n` entries of 4 bytes of `buf` from entry `at` on, as a tensor of their own (an allocation takes 0.7 us, this 0.2).
+at::Tensor part(const at::Tensor& buf, at::ScalarType type, int64_t at, int64_t n) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buf.storage()), buf.key_set(), c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  return t;
+}
+
 // The given stream made current for the call, so that what it allocates belongs to it.
 struct OnStream {
   std::optional<c10::cuda::CUDAStreamGuard> guard;
@@ -104,10 +112,13 @@ py::tuple add_rmsnorm_quant_act(const at::Tensor& x, const at::Tensor& residual,
     throw py::value_error("residual_out must have the shape of x");
   }
   at::Tensor q, s, sq;
-  if (out)
+  if (out) {
     std::tie(q, s, sq) = *out;
-  else
-    q = make(dev, {T, K}, at::kChar), s = make(dev, {T}, at::kFloat), sq = make(dev, {T}, at::kInt);
+  } else {
+    const int64_t second = (T + 3) / 4 * 4;  // 16-byte aligned
+    const at::Tensor rows = make(dev, {second + T}, at::kInt);
+    q = make(dev, {T, K}, at::kChar), s = part(rows, at::kFloat, 0, T), sq = part(rows, at::kInt, second, T);
+  }
   check(api.add_norm(arg(dev, "x", x, x.scalar_type(), n), xt, arg(dev, "residual", residual, residual.scalar_type(), n), rt,
                      gain ? reinterpret_cast<const float*>(arg(dev, "gain", *gain, at::kFloat, K)) : nullptr, (float)eps, T, K,
                      arg(dev, "residual_out", *residual_out, residual.scalar_type(), n),
@@ -133,8 +144,9 @@ py::tuple paged_plan(const at::Tensor& new_lens, const at::Tensor& ctx_lens, con
       for (const at::Tensor* i : {&new_lens, &ctx_lens, &n_free})
         if (o->numel() > 0 && i->numel() > 0 && o->data_ptr() == i->data_ptr()) throw py::value_error("no output may be an input");
   } else {
-    cu = make(dev, {B + 1}, at::kInt), kv = make(dev, {B}, at::kInt), pos = make(dev, {T}, at::kInt), slots = make(dev, {T}, at::kInt);
-    left = make(dev, {1}, at::kInt);
+    const at::Tensor buf = make(dev, {2 * B + 2 + 2 * T}, at::kInt);  // 4-byte alignment is all that the step's calls need
+    cu = part(buf, at::kInt, 0, B + 1), kv = part(buf, at::kInt, B + 1, B), pos = part(buf, at::kInt, 2 * B + 1, T);
+    slots = part(buf, at::kInt, 2 * B + 1 + T, T), left = part(buf, at::kInt, 2 * B + 1 + 2 * T, 1);
   }
   check(api.plan(ints(dev, "new_lens", new_lens, B), ints(dev, "ctx_lens", ctx_lens, B), B, page_size,
                  ints(dev, "block_table", block_table, B * width), width, ints(dev, "free_pages", free_pages, n_list), n_list,

@@ -54,6 +54,26 @@ def test_plan(B, P, new_max, ctx_max, pad):
     assert tb.device_status() == 0
 
 
+def test_plan_outputs_are_tensors_of_their_own():
+    """Parts of one allocation: ordinary tensors for torch, alive as long as any of them is."""
+    new, ctx = torch.tensor([3, 1], **I32), torch.tensor([0, 16], **I32)
+    table = torch.tensor([[-1, -1], [4, -1]], **I32)
+    free, n = torch.arange(4, **I32), torch.tensor([4], **I32)
+    cu, kv, pos, slots, left = tb.paged_plan(new, ctx, table, free, n, 16, 5)
+    assert [tuple(t.shape) for t in (cu, kv, pos, slots, left)] == [(3,), (2,), (5,), (5,), (1,)]
+    assert all(t.is_contiguous() and t.dtype == torch.int32 for t in (cu, kv, pos, slots, left))
+    n.copy_(left)
+    ctx.copy_(kv)
+    del cu, kv, left
+    junk = [torch.full((64,), -5, **I32) for _ in range(20)]
+    assert pos.tolist() == [0, 1, 2, 16, 0] and (slots + 1).tolist() == [49, 50, 51, 33, 0] and pos.clone().sum() == 19
+    assert n.item() == 2 and ctx.tolist() == [3, 17] and len(junk) == 20
+    res, q, s, sq = tb.add_rmsnorm_quant_act(torch.ones(3, 64, device=DEV), torch.ones(3, 64, device=DEV), None)
+    assert s.data_ptr() % 16 == 0 and sq.data_ptr() % 16 == 0 and s.dtype == torch.float32 and sq.dtype == torch.int32
+    s.mul_(2)
+    assert sq.tolist() == [64 * 127] * 3 and s.tolist() == [127.0] * 3
+
+
 def test_plan_takes_the_top_of_the_list_only():
     new, ctx, P = [17, 0, 1], [0, 5, 16], 16
     table, free, _ = _plan_inputs(new, ctx, P, extra_free=9)
