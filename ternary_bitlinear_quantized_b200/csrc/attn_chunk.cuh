@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
   pdl_launch_dependents();
   pdl_wait();
   PagedWalk<ChunkTiles> w;
-  w.begin(a, gridDim.x, &s_walk);
+  w.begin<PC_THREADS>(a, gridDim.x, &s_walk);
   if (threadIdx.x == 0) a.desc[blockIdx.x].first = -1;
 
   if (warp < 8) {

@@ -133,14 +133,15 @@ struct PagedWalk {
   // The descriptor of this tile, which began in another CTA's share.
   BN_DEV PagedTile ended() const { return {(int)div_nonneg(pos - at + Tiles::FIXED, per), t0, n, head, tile}; }
 
-  // Block-wide: finds the CTA's share.  Up to blockDim requests are taken at once, S threads of one
+  // Block-wide: finds the CTA's share.  Up to THREADS requests are taken at once, S threads of one
   // warp (a power of two) per request, each with q consecutive tiles of one head; prefix sums over
   // the threads give the place of each request (times Hkv) and of each thread's tiles in a head.
+  template <int THREADS>
   BN_DEV void begin(const PagedArgs& a, int C, PagedWalkShared* sm) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int logS = 0;
-    while (logS < 5 && (a.B << (logS + 1)) <= (int)blockDim.x) ++logS;
-    const int S = 1 << logS, sub = threadIdx.x & (S - 1), per_round = blockDim.x >> logS;
+    while (logS < 5 && (a.B << (logS + 1)) <= THREADS) ++logS;
+    const int S = 1 << logS, sub = threadIdx.x & (S - 1), per_round = THREADS >> logS;
     bool bad = false;
     int rt0, rn, rkv, j0, j1;  // this thread's request and tiles of the last round
     auto mine_of = [&](int i) {
@@ -168,7 +169,8 @@ struct PagedWalk {
       if (lane == 31) sm->warp_sum[warp] = v;
       __syncthreads();
       all = 0;
-      for (int k = 0; k < nw; ++k) {
+#pragma unroll
+      for (int k = 0; k < THREADS / 32; ++k) {
         const long long x = sm->warp_sum[k];
         if (k < warp) v += x;
         all += x;
@@ -297,7 +299,7 @@ __global__ void __launch_bounds__(PD_THREADS, 2) k_attn_paged_few(const PagedArg
   pdl_launch_dependents();
   pdl_wait();
   PagedWalk<FewTiles> w;
-  w.begin(a, gridDim.x, &s_walk);
+  w.begin<PD_THREADS>(a, gridDim.x, &s_walk);
   if (threadIdx.x == 0) a.desc[blockIdx.x].first = -1;
   const uint32_t ring = smem_addr(pd_sm) + warp * PD_STAGES * PD_STAGE_BYTES;
   const int g = lane >> 2, tq = lane & 3;
