@@ -1344,7 +1344,7 @@ static bool make_map_heads(CUtensorMap* m, const void* base, int64_t d1, int64_t
 // 32 rows 70 against 60 us, 48 rows 134 against 61 us; one request behind 8192 rows, 5 heads, 32 rows:
 // 18 against 24 us.
 constexpr int64_t PAGED_FEW_ROWS = 32;
-static bool paged_few(int64_t G, int64_t max_new) { return max_new * G <= PAGED_FEW_ROWS; }
+static bool paged_few(int64_t G, int64_t max_new) { return max_new <= PAGED_FEW_ROWS / G; }
 static int paged_ctas(bool few) { return (few ? 2 : 1) * device_sm_count(); }
 
 // The workspace: a tile descriptor and two partial tiles per CTA.

@@ -78,6 +78,9 @@ def test_attention_refusals(L):
     for c in (dict(T=0), dict(B=0), dict(max_new=0)):
         assert _call(f, a, q=None, **c) == 0
     assert L.bitnet_attention_paged_workspace_bytes(5, 2, 1) == 0 and L.bitnet_attention_paged_workspace_bytes(4, 2, -1) == 0
+    # the most rows there are take the workspace of the kernel for many rows, as 33 of one head do
+    assert L.bitnet_attention_paged_workspace_bytes(4, 2, 1 << 62) == L.bitnet_attention_paged_workspace_bytes(1, 1, 33)
+    assert L.bitnet_attention_paged_workspace_bytes(1, 1, 33) > L.bitnet_attention_paged_workspace_bytes(1, 1, 32) > 0
     assert L.bitnet_status_string(8) != b"unknown status"
 
 
