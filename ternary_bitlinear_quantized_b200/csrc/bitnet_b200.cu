@@ -1309,19 +1309,19 @@ bitnet_status bitnet_rope_paged_append(const void* q, const void* k, const void*
   long double g = 1.0L / 6.283185307179586476925286766559L;
   for (int i = 0; i < PG_D / 2; ++i, g *= step) turns.g[i] = (double)g;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // four tokens per CTA once that still gives every SM two CTAs
-  const int tok = T >= 8 * device_sm_count() ? 4 : 1;
+  // several tokens per CTA once that still gives every SM four CTAs
+  const int tok = T >= 4 * ROPE_TOKENS * device_sm_count() ? ROPE_TOKENS : 1;
   auto run = [&](auto* x, auto* kern) {
     typedef decltype(x) P;
-    return launch(kern, dim3((unsigned)((T + tok - 1) / tok)), dim3(ROPE_THREADS), 0, s, true, (P)q, (P)k, (P)v, positions, slots, (int)T,
+    return launch(kern, dim3((unsigned)((T + tok - 1) / tok)), dim3((unsigned)rope_threads(tok)), 0, s, true, (P)q, (P)k, (P)v, positions, slots, (int)T,
                   (int)Hq, (int)Hkv, page_log2(page_size), (long long)(n_pages * page_size), turns,
                   reinterpret_cast<__nv_bfloat16*>(q_rot), reinterpret_cast<__nv_bfloat16*>(k_pages),
                   reinterpret_cast<__nv_bfloat16*>(v_pages));
   };
   const __nv_bfloat16* xb = nullptr;
   const float* xf = nullptr;
-  const cudaError_t e = xt == BITNET_BF16 ? (tok == 4 ? run(xb, k_rope_paged<__nv_bfloat16, 4>) : run(xb, k_rope_paged<__nv_bfloat16, 1>))
-                                          : (tok == 4 ? run(xf, k_rope_paged<float, 4>) : run(xf, k_rope_paged<float, 1>));
+  const cudaError_t e = xt == BITNET_BF16 ? (tok > 1 ? run(xb, k_rope_paged<__nv_bfloat16, ROPE_TOKENS>) : run(xb, k_rope_paged<__nv_bfloat16, 1>))
+                                          : (tok > 1 ? run(xf, k_rope_paged<float, ROPE_TOKENS>) : run(xf, k_rope_paged<float, 1>));
   return e == cudaSuccess ? BITNET_OK : cuda_fail(e, "k_rope_paged");
 }
 

@@ -201,29 +201,31 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const int* __restri
 //
 // Bound by HBM: each value is read and written once.  A CTA takes TOKENS tokens: their 64
 // angles each are made once and shared by all heads (a sine and cosine per head would cost more
-// than the copy), then every thread moves 8 + 8 values of one head for all the tokens at once, eight
-// 16-byte loads in flight.  8400 tokens of 64 + 8 + 8 heads: 60.7 us (5.7 TB/s); one token at a time 62 us.
-// With few tokens each has a CTA of its own: 64 tokens 4.1 us, four per CTA 7.2 us.
-constexpr int ROPE_THREADS = 128;
+// than the copy), then every thread moves 8 + 8 values of one head for all the tokens at once, 2 TOKENS
+// 16-byte loads in flight.  8400 tokens of 64 + 8 + 8 heads: 57.5 us (6.0 TB/s) with two tokens and 128 threads
+// a CTA, 58.5 with four (cosines read one by one: 60.7), 62 us one token after the other.  With few
+// tokens each has a CTA of 256 threads: 64 tokens 3.5 us, of 128 threads 4.1, four tokens per CTA 7.2.
+constexpr int ROPE_TOKENS = 2;
+BN_HOST_DEV constexpr int rope_threads(int tokens) { return tokens == 1 ? 256 : 128; }
 struct RopeTurns {
   double g[PG_D / 2];
 };
 template <typename TIn, int TOKENS>
-__global__ void __launch_bounds__(ROPE_THREADS) k_rope_paged(const TIn* __restrict__ q, const TIn* __restrict__ k,
+__global__ void __launch_bounds__(rope_threads(TOKENS)) k_rope_paged(const TIn* __restrict__ q, const TIn* __restrict__ k,
                                                              const TIn* __restrict__ v, const int* __restrict__ positions,
                                                              const int* __restrict__ slots, int T, int Hq, int Hkv, int log2P,
                                                              long long n_slots, const __grid_constant__ RopeTurns turns,
                                                              __nv_bfloat16* __restrict__ q_rot,
                                                              __nv_bfloat16* __restrict__ k_pages,
                                                              __nv_bfloat16* __restrict__ v_pages) {
-  constexpr int HALF = PG_D / 2;
-  __shared__ float s_cos[TOKENS][HALF], s_sin[TOKENS][HALF];
+  constexpr int HALF = PG_D / 2, THREADS = rope_threads(TOKENS);
+  __shared__ __align__(16) float s_cos[TOKENS][HALF], s_sin[TOKENS][HALF];
   __shared__ int s_slot[TOKENS];
   pdl_launch_dependents();
   pdl_wait();
   const int t0 = blockIdx.x * TOKENS;
 #pragma unroll
-  for (int a0 = 0; a0 < TOKENS * HALF; a0 += ROPE_THREADS) {
+  for (int a0 = 0; a0 < TOKENS * HALF; a0 += THREADS) {
     const int tt = (a0 + threadIdx.x) / HALF, i = threadIdx.x % HALF, t = t0 + tt;
     const int slot = tt < TOKENS && t < T ? __ldg(slots + t) : -1;
     if (i == 0 && tt < TOKENS) {
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope_paged(const TIn* __restri
     return *reinterpret_cast<const uint32_t*>(&w);
   };
   const int units = (Hq + 2 * Hkv) * 8;  // (head, 8-value chunk of its lower half with the chunk 64 above)
-  for (int u = threadIdx.x; u < units; u += ROPE_THREADS) {
+  for (int u = threadIdx.x; u < units; u += THREADS) {
     const int hh = u >> 3, c = (u & 7) * 8;
     const bool is_q = hh < Hq, is_v = hh >= Hq + Hkv;
     const int h = is_q ? hh : hh - Hq - (is_v ? Hkv : 0), heads = is_q ? Hq : Hkv;
@@ -262,9 +264,15 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope_paged(const TIn* __restri
       lo[tt].get(a);
       hi[tt].get(b);
       if (!is_v) {
+        float cs[8], sn[8];
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          *reinterpret_cast<float4*>(cs + j) = *reinterpret_cast<const float4*>(&s_cos[tt][c + j]);
+          *reinterpret_cast<float4*>(sn + j) = *reinterpret_cast<const float4*>(&s_sin[tt][c + j]);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float co = s_cos[tt][c + j], si = s_sin[tt][c + j], x1 = a[j], x2 = b[j];
+          const float co = cs[j], si = sn[j], x1 = a[j], x2 = b[j];
           a[j] = __fsub_rn(__fmul_rn(x1, co), __fmul_rn(x2, si));
           b[j] = __fadd_rn(__fmul_rn(x2, co), __fmul_rn(x1, si));
         }
