@@ -201,13 +201,17 @@ static bitnet_status enqueue_quant(const void* x, bitnet_dtype xt, const float* 
 }
 
 // Residual addition in front of the norm.  Rows that fit 16 warps' registers: 32 values a thread
-// with many rows, 8 (with up to eight warps) where there are too few rows to fill the GPU and a
-// row's own latency counts.  Longer rows go by way of shared memory.
+// with many rows, fewer (8 and up) and more warps where there are too few rows to fill the GPU and a
+// row's own latency counts: 333 rows of 2560 4.3 us with 16 values a thread, 5.0 with 32; 256 rows of
+// 5120 5.2 us with 16 warps a row, 7.0 with 8 (333 rows, no longer one wave of two CTAs an SM, 8.3
+// against 7.3).  Longer rows go by way of shared memory.
 template <typename TIn, typename TRes, bool ALIGNED>
 static cudaError_t launch_add_quant(const TIn* x, const TRes* r_in, TRes* r_out, const float* gain, float eps, int64_t T, int64_t K,
                                     int8_t* q, float* s_x, int32_t* sum_q, cudaStream_t s) {
-  const int64_t places = K + (ALIGNED ? 0 : 7), per_warp = T <= 256 ? 256 : 1024;
-  const int w = places <= per_warp ? 1 : (places <= 2 * per_warp ? 2 : (places <= 4 * per_warp ? 4 : (places <= 8 * 1024 ? 8 : 16)));
+  const int sms = device_sm_count();
+  const int64_t places = K + (ALIGNED ? 0 : 7), per_warp = T <= 2 * sms ? 256 : (T <= 4 * sms ? 512 : 1024);
+  int w = places <= per_warp ? 1 : (places <= 2 * per_warp ? 2 : (places <= 4 * per_warp ? 4 : 8));
+  if (places > 8 * 1024 || (places > 8 * 512 && T <= 2 * sms)) w = 16;
   const int threads = qw_threads(w), rows = threads / 32 / w;
   auto* kern = w == 1   ? k_add_rmsnorm_quant<TIn, TRes, 1, ALIGNED>
                : w == 2 ? k_add_rmsnorm_quant<TIn, TRes, 2, ALIGNED>
