@@ -167,8 +167,9 @@ BN_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
 // bits of z + 1.5 2^23), 2^f on [-1/2, 1/2] as a polynomial of degree 5 through 1 at 0 (its
 // coefficients fitted here for the least largest relative error, 2^-23.4), n added to the exponent.
 // Values below -127 and -inf give exactly 0.  Every fourth pair of weights goes this way: at 16
-// exponentials per cycle and SM they bound the softmax; with a quarter of the pairs moved, four
-// prompts' chunks at the 70B shape took 809 us against 826, with three eighths 847 (issue slots).
+// exponentials per cycle and SM they bound the softmax.  Four prompts' chunks at the 70B shape, calls
+// without a pause: 757 us with a quarter of the pairs moved, 778 with an eighth, 792 with none; with
+// three eighths (measured earlier) 5 % more than with a quarter, for want of issue slots.
 BN_DEV void exp2_pair(uint64_t z, float& x, float& y) {
   unpack_f32x2(z, x, y);
   z = pack_f32x2(fmaxf(x, -127.0f), fmaxf(y, -127.0f));

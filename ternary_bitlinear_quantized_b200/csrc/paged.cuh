@@ -14,7 +14,6 @@
 namespace bitnet {
 
 constexpr int PG_D = 128;               // head size
-constexpr int PG_MAX_REQUESTS = 4096;   // k_paged_plan keeps two prefix sums of this many requests in shared memory
 
 BN_DEV void flag_index_error() { atomicExch(&g_device_status, (int)BITNET_ERR_INDEX); }
 
@@ -74,7 +73,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const int* __restri
                                                              const int* __restrict__ n_free, int T, int* __restrict__ cu_out,
                                                              int* __restrict__ kv_out, int* __restrict__ pos_out,
                                                              int* __restrict__ slot_out, int* __restrict__ n_free_out) {
-  extern __shared__ int plan_sm[];
+  extern __shared__ int plan_sm[];  // two sums of B + 1 requests: 32 KB for BITNET_MAX_REQUESTS
   __shared__ long long scratch[64];
   int* cu = plan_sm;            // [B + 1] tokens before request i
   int* start = plan_sm + B + 1; // [B + 1] new pages before request i
