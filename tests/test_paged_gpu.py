@@ -536,6 +536,67 @@ def test_attention_decode_agrees_with_the_contiguous_cache():
     assert ((got.double() - want.double()).abs() <= 2 * bound + A * 2.0 ** -15).all()
 
 
+# ------------------------------------------------------------------------------------------- refusals
+
+def _refused(status, fn, *args, **kw):
+    """ValueError for what the binding checks, BitnetError with its status for what the library does."""
+    with pytest.raises(ValueError if status is None else tb.BitnetError) as e:
+        fn(*args, **kw)
+    if status is not None:
+        assert e.value.status == status
+
+
+def test_refusals_of_the_binding():
+    b = Batch([2, 1], [20, 33], 4, 2, 16)
+    att = (b.q, b.kp, b.vp, b.table, b.cu, b.kv, 2)
+
+    def swap(i, x):
+        return (*att[:i], x, *att[i + 1:])
+
+    _refused(None, tb.attention_paged, *swap(0, b.q.float()))
+    _refused(None, tb.attention_paged, *swap(0, b.q.transpose(0, 1)))
+    _refused(None, tb.attention_paged, *swap(0, b.q[0]))
+    _refused(None, tb.attention_paged, *swap(1, b.kp[:, :1].contiguous()))
+    _refused(None, tb.attention_paged, *swap(2, b.vp.float()))
+    _refused(None, tb.attention_paged, *swap(3, b.table.long()))
+    _refused(None, tb.attention_paged, *swap(3, b.table[:, ::2]))
+    _refused(None, tb.attention_paged, *swap(4, b.cu[:-1]))
+    _refused(None, tb.attention_paged, *swap(5, b.kv.cpu()))
+    _refused(None, tb.attention_paged, *att, out_dtype=torch.float16)
+    _refused(None, tb.attention_paged, *att, out=torch.empty(1, 4, D, device=DEV))
+    _refused(2, tb.attention_paged, *swap(6, -1))
+    _refused(5, tb.attention_paged, *att, ws=torch.empty(64, dtype=torch.uint8, device=DEV))
+    _refused(3, tb.attention_paged, *att, ws=torch.empty(1 << 26, dtype=torch.uint8, device=DEV)[1:])
+    k, v, pos, slots = b.q[:, :2].contiguous(), b.q[:, 2:].contiguous(), torch.zeros(3, **I32), torch.arange(3, **I32)
+    rope = (b.q, k, v, pos, slots, 1e4, b.kp.clone(), b.vp.clone())
+    _refused(None, tb.rope_paged_append, b.q, k.float(), *rope[2:])
+    _refused(None, tb.rope_paged_append, b.q, k, v[:2], *rope[3:])
+    _refused(None, tb.rope_paged_append, *rope[:3], pos[:2], *rope[4:])
+    _refused(None, tb.rope_paged_append, *rope, q_rot=torch.empty(3, 4, D, device=DEV))
+    _refused(2, tb.rope_paged_append, *rope[:5], 0.0, *rope[6:])
+    _refused(2, tb.rope_paged_append, *rope[:6], b.kp[:, :, :8].contiguous(), b.vp[:, :, :8].contiguous())
+    new, ctx, free, n = torch.ones(2, **I32), torch.zeros(2, **I32), torch.arange(4, **I32), torch.tensor([4], **I32)
+    plan = (new, ctx, torch.full((2, 2), -1, **I32), free, n, 16, 2)
+    outs = [torch.empty(s, **I32) for s in (3, 2, 2, 2, 1)]
+    _refused(None, tb.paged_plan, *plan, out=(*outs[:4], n))
+    _refused(None, tb.paged_plan, *plan, out=(outs[0], ctx, *outs[2:]))
+    _refused(None, tb.paged_plan, *plan, out=(outs[0], outs[1], outs[2][:1], *outs[3:]))
+    _refused(None, tb.paged_plan, new[:1], *plan[1:])
+    _refused(2, tb.paged_plan, *plan[:5], 24, 2)
+    _refused(2, tb.paged_plan, *plan[:6], -1)
+    x = torch.ones(2, 64, device=DEV)
+    _refused(None, tb.add_rmsnorm_quant_act, x, x.half(), None)
+    _refused(None, tb.add_rmsnorm_quant_act, x, x[:1], None)
+    _refused(None, tb.add_rmsnorm_quant_act, x, x.t().contiguous().t(), None)
+    _refused(None, tb.add_rmsnorm_quant_act, x, x, x[0, :32])
+    _refused(None, tb.add_rmsnorm_quant_act, x, x, None, residual_out=x.bfloat16())
+    _refused(2, tb.add_rmsnorm_quant_act, x[:, :0].contiguous(), x[:, :0].contiguous(), None)
+    y = torch.ones(129, device=DEV)[1:].view(2, 64)
+    _refused(3, tb.add_rmsnorm_quant_act, y, x, None)
+    assert tb.device_status() == 0
+    check_attention(b, tb.attention_paged(*att), p_round=weight_step(b))
+
+
 # ------------------------------------------------------------------------------------------- a block together
 
 @pytest.mark.parametrize("new,ctx", [([1, 1, 1], [40, 0, 333]), ([70, 1, 19, 0], [5, 400, 0, 64])])
