@@ -393,7 +393,9 @@ size_t bitnet_attention_paged_workspace_bytes(int64_t Hq, int64_t Hkv, int64_t m
  * tokens are left as they were; cache rows at and behind kv_lens[i] may hold anything.  A
  * non-finite value in a visible row makes the outputs of that request and head undefined, of
  * no other.  Scores, maxima, sums and outputs are held in fp32; the weights enter the product with v
- * as bf16 (as the sum of two bf16 where max_new * Hq / Hkv <= 32).  Equal calls give equal bits.  A request whose lengths do not
+ * as the sum of two bf16 (2^-16 of each) where out is fp32 or max_new * Hq / Hkv <= 32, else as one
+ * bf16 (2^-8, below the output's own rounding).  So fp32 outputs are as precise in a step that holds a chunk as in
+ * a decode step.  Equal calls give equal bits.  A request whose lengths do not
  * fit the call (cu_new descending or beyond T, more than max_new tokens, kv_lens beyond the
  * table) is skipped; a page id outside [0, n_pages) counts as a page of zeros; both set
  * BITNET_ERR_INDEX.  Two calls that share a workspace must not run concurrently.

@@ -458,7 +458,8 @@ def attention_paged(q_rot, k_pages, v_pages, block_table, cu_new, kv_lens, max_n
                     out=None, ws=None, stream=None) -> torch.Tensor:
     """Causal GQA attention of q_rot (bf16 [T, Hq, 128]), the new tokens of B requests back to back (request i:
     rows cu_new[i] .. cu_new[i + 1] - 1, at most max_new), over each request's pages.  Rows of ``out`` behind the
-    last request are left as they were."""
+    last request are left as they were.  fp32 outputs keep the weights to 2^-16 in every step, bf16 ones to a bf16
+    where max_new * Hq / Hkv > 32."""
     return (_native or _load_serving()).attention_paged(q_rot, k_pages, v_pages, block_table, cu_new, kv_lens, max_new, out_dtype,
                                                    out, ws, stream)
 

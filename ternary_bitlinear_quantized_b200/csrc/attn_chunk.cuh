@@ -8,7 +8,7 @@
 //   warp 10         TMA loads of K, page by page, into a ring of two 32 KB slots
 //   warp 11         TMA loads of Q, and of V into another ring
 // A unit is done in two steps of 64 cache rows.  Tensor memory (512 columns): each half has S of both
-// steps (64 columns each, of which P takes the first 32 once the scores are in registers) and O
+// steps (64 columns each, of which P takes the first 32, or all, once the scores are in registers) and O
 // (128).  So the scores of the next step are there while the softmax works on this one's, and a
 // half waits for neither the other half nor its own products.
 //
@@ -21,8 +21,12 @@
 //
 // The running maximum of a row moves only when the scores outgrow it by 2^8: until then the weights
 // are at most 2^8, which fp32 sums and bf16's exponent hold without loss, and O needs no rescaling.
-// The weights are rounded to bf16 for the second product (the tensor core's operand type; half a
-// step is 2^-8 of each weight); the row sum adds the unrounded weights in fp32.
+// The weights enter the second product as bf16, the tensor core's operand type; the row sum adds the
+// unrounded weights in fp32.  For bf16 outputs one bf16 a weight: half a step is 2^-8 of each, which the
+// output's own half step outweighs (four chunks at the 70B shape, error against 64 bits 0.00168 where
+// unrounded weights give 0.00167).  For fp32 outputs (SPLIT) two: the weight rounded and what that left
+// over, 2^-16, in the columns that the scores leave free, and a second product over the same V: the four
+// chunks 857-900 us instead of 711-772 with one bf16, a 500-token chunk of 20/5 heads 42.5 instead of 37.2.
 //
 // Pages that no row sees and page ids out of range are loaded as zeros (a page coordinate beyond
 // the tensor: the copy fills zeros).  Rows at and behind kv in the last page may hold anything: their
@@ -211,10 +215,12 @@ BN_DEV void pc_scores(int h, uint32_t q, uint32_t k) {
   umma_bf16_ss<off, off + B * 512>(h * 128 + B * 64, q, k, KK > 0);
   if constexpr (KK < 7) pc_scores<B, KK + 1>(h, q, k);
 }
-template <int B, int KK = 0>
+// SPLIT: the second bf16 of the weights in the 32 columns behind the first.
+template <bool SPLIT, int B, int KK = 0>
 BN_DEV void pc_values(int h, uint32_t v, bool first) {
   umma_bf16_ts<(B * 4 + KK) * 128>(256 + h * 128, h * 128 + B * 64 + KK * 8, v, !first);
-  if constexpr (KK < 3) pc_values<B, KK + 1>(h, v, false);
+  if constexpr (SPLIT) umma_bf16_ts<(B * 4 + KK) * 128>(256 + h * 128, h * 128 + B * 64 + 32 + KK * 8, v, 1);
+  if constexpr (KK < 3) pc_values<SPLIT, B, KK + 1>(h, v, false);
 }
 // First row of unit u behind kv if it lies inside a page of that unit (whose rows from there on may
 // hold anything), else 0.
@@ -223,6 +229,8 @@ BN_DEV int pc_tail(const PagedArgs& a, int kv, int u) {
   return tail > 0 && tail < PC_U && (tail & (a.P - 1)) ? tail : 0;
 }
 
+// SPLIT: fp32 outputs; otherwise bf16 ones.
+template <bool SPLIT>
 __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid_constant__ PagedMaps maps, const PagedArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) unsigned long long s_bars[2 * PC_KSLOTS + 3 * PC_VSLOTS + 11];
@@ -350,7 +358,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
             uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
             for (int c = 0; c < 64; c += 32) {
-              uint32_t p[16];
+              uint32_t p[16], left[SPLIT ? 16 : 1];
 #pragma unroll
               for (int k = 0; k < 32; k += 2) {
                 float x, y;
@@ -362,9 +370,12 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
                   y = exp2_approx(y);
                 }
                 sum2[(k >> 1) & 1] = add_f32x2(sum2[(k >> 1) & 1], pack_f32x2(x, y));
-                p[k >> 1] = pack_bf16(x, y);
+                const uint32_t w = pack_bf16(x, y);
+                p[k >> 1] = w;
+                if constexpr (SPLIT) left[k >> 1] = pack_bf16(__fsub_rn(x, __uint_as_float(w << 16)), __fsub_rn(y, __uint_as_float(w & 0xFFFF0000u)));
               }
               tmem_st16(tS + 64 * b + (c >> 1), p);
+              if constexpr (SPLIT) tmem_st16(tS + 64 * b + 32 + (c >> 1), left);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -384,7 +395,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
           // By way of shared memory, so that a warp writes whole 128-byte lines: 32 rows of 128 bytes
           // (64 bf16 or 32 fp32 columns), their 16-byte chunks permuted by the row.
           const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);  // NaN stays
-          const bool bf = a.out_dtype == BITNET_BF16;
+          constexpr bool bf = !SPLIT;
           const long long off = r.there ? ((long long)(w.t0 + r.t) * a.Hq + w.head * a.G + r.g) * (bf ? PG_D * 2 : PG_D * 4) : -1;
           const uint32_t stage = sV + PC_VSLOTS * PC_TILE_BYTES + warp * 4096;
           long long to[8];  // of the rows whose chunk lane & 7 this lane writes
@@ -476,7 +487,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
             if (have) ok = mbar_wait_bounded(p_full(h, 0), ph_p);
             if (!ok) break;
             tc_fence_after();
-            if (have) pc_values<0>(h, v, it == 0);
+            if (have) pc_values<SPLIT, 0>(h, v, it == 0);
             if (more) pc_scores<0>(h, q, k);
             umma_commit(s_full(h, 0));
             if (have) {
@@ -484,7 +495,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1) k_attn_paged_chunk(const __grid
               if (!ok) break;
               ph_p ^= 1u;
               tc_fence_after();
-              pc_values<1>(h, v, false);
+              pc_values<SPLIT, 1>(h, v, false);
             }
             if (more) pc_scores<1>(h, q, k);
           }

@@ -1426,9 +1426,10 @@ bitnet_status bitnet_attention_paged(const void* q_rot, const void* k_pages, con
       !make_map_heads(&maps.v, v_pages, page_size, Hkv, n_pages, rows, 1) ||
       !make_map_heads(&maps.q, q_rot, a.G, Hkv, T, a.GB, a.TB))
     return cuda_fail(cudaErrorUnknown, "cuTensorMapEncodeTiled (pages)");
-  e = opt_in_smem((const void*)k_attn_paged_chunk, 15);
+  auto* chunk = ot == BITNET_F32 ? k_attn_paged_chunk<true> : k_attn_paged_chunk<false>;
+  e = opt_in_smem((const void*)chunk, ot == BITNET_F32 ? 13 : 15);
   if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_chunk attribute");
-  e = launch(k_attn_paged_chunk, dim3((unsigned)ctas), dim3(PC_THREADS), PC_SMEM, s, true, maps, a);
+  e = launch(chunk, dim3((unsigned)ctas), dim3(PC_THREADS), PC_SMEM, s, true, maps, a);
   if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_chunk");
   e = launch(k_attn_paged_chunk_join, dim3((unsigned)ctas, PG_D / (4 * PC_JOIN_V4)), dim3(PC_M), 0, s, true, a);
   if (e != cudaSuccess) return cuda_fail(e, "k_attn_paged_chunk_join");
