@@ -49,6 +49,19 @@ void check(bitnet_status st, const char* where) {
   throw py::error_already_set();
 }
 
+// The work of a call without the interpreter's lock: an allocation may wait for the device, and a launch for room in the
+// stream's queue, which another Python thread or a host callback in that stream may have to make.  What `f` throws
+// are C++ exceptions until the lock is held again.
+template <typename F>
+void unlocked(const char* where, F f) {
+  bitnet_status st;
+  {
+    const py::gil_scoped_release release;
+    st = f();
+  }
+  check(st, where);
+}
+
 // The call's device: that of its first tensor, which has to be the current one.
 int device_of(const at::Tensor& t, const char* name) {
   if (!t.is_cuda() || t.get_device() != c10::cuda::current_device())
@@ -101,30 +114,31 @@ typedef std::optional<at::Tensor> Maybe;
 py::tuple add_rmsnorm_quant_act(const at::Tensor& x, const at::Tensor& residual, const Maybe& gain, double eps, Maybe residual_out,
                                 const std::optional<std::tuple<at::Tensor, at::Tensor, at::Tensor>>& out, const py::object& stream) {
   const OnStream on(stream);
-  const int dev = device_of(x, "x");
-  dims("x", x, 2);
-  const int64_t T = x.size(0), K = x.size(1), n = T * K;
-  const bitnet_dtype xt = float_code("x", x), rt = float_code("residual", residual);
-  if (residual.sizes() != x.sizes()) throw py::value_error("residual must have the shape of x");
-  if (!residual_out) {
-    residual_out = make(dev, {T, K}, residual.scalar_type());
-  } else if (residual_out->sizes() != x.sizes()) {
-    throw py::value_error("residual_out must have the shape of x");
-  }
   at::Tensor q, s, sq;
-  if (out) {
-    std::tie(q, s, sq) = *out;
-  } else {
-    const int64_t second = (T + 3) / 4 * 4;  // 16-byte aligned
-    const at::Tensor rows = make(dev, {second + T}, at::kInt);
-    q = make(dev, {T, K}, at::kChar), s = part(rows, at::kFloat, 0, T), sq = part(rows, at::kInt, second, T);
-  }
-  check(api.add_norm(arg(dev, "x", x, x.scalar_type(), n), xt, arg(dev, "residual", residual, residual.scalar_type(), n), rt,
-                     gain ? reinterpret_cast<const float*>(arg(dev, "gain", *gain, at::kFloat, K)) : nullptr, (float)eps, T, K,
-                     arg(dev, "residual_out", *residual_out, residual.scalar_type(), n),
-                     reinterpret_cast<int8_t*>(arg(dev, "q", q, at::kChar, n)), reinterpret_cast<float*>(arg(dev, "s_x", s, at::kFloat, T)),
-                     ints(dev, "sum_q", sq, T), on.get(dev)),
-        "add_rmsnorm_quant_act");
+  unlocked("add_rmsnorm_quant_act", [&] {
+    const int dev = device_of(x, "x");
+    dims("x", x, 2);
+    const int64_t T = x.size(0), K = x.size(1), n = T * K;
+    const bitnet_dtype xt = float_code("x", x), rt = float_code("residual", residual);
+    if (residual.sizes() != x.sizes()) throw py::value_error("residual must have the shape of x");
+    if (!residual_out) {
+      residual_out = make(dev, {T, K}, residual.scalar_type());
+    } else if (residual_out->sizes() != x.sizes()) {
+      throw py::value_error("residual_out must have the shape of x");
+    }
+    if (out) {
+      std::tie(q, s, sq) = *out;
+    } else {
+      const int64_t second = (T + 3) / 4 * 4;  // 16-byte aligned
+      const at::Tensor rows = make(dev, {second + T}, at::kInt);
+      q = make(dev, {T, K}, at::kChar), s = part(rows, at::kFloat, 0, T), sq = part(rows, at::kInt, second, T);
+    }
+    return api.add_norm(arg(dev, "x", x, x.scalar_type(), n), xt, arg(dev, "residual", residual, residual.scalar_type(), n), rt,
+                       gain ? reinterpret_cast<const float*>(arg(dev, "gain", *gain, at::kFloat, K)) : nullptr, (float)eps, T, K,
+                       arg(dev, "residual_out", *residual_out, residual.scalar_type(), n),
+                       reinterpret_cast<int8_t*>(arg(dev, "q", q, at::kChar, n)), reinterpret_cast<float*>(arg(dev, "s_x", s, at::kFloat, T)),
+                       ints(dev, "sum_q", sq, T), on.get(dev));
+  });
   return py::make_tuple(*residual_out, q, s, sq);
 }
 
@@ -133,26 +147,27 @@ py::tuple paged_plan(const at::Tensor& new_lens, const at::Tensor& ctx_lens, con
                      const std::optional<std::tuple<at::Tensor, at::Tensor, at::Tensor, at::Tensor, at::Tensor>>& out,
                      const py::object& stream) {
   const OnStream on(stream);
-  const int dev = device_of(new_lens, "new_lens");
-  dims("block_table", block_table, 2);
-  const int64_t B = block_table.size(0), width = block_table.size(1), n_list = free_pages.numel();
-  if (T < 0) check(BITNET_ERR_SHAPE, "paged_plan");
   at::Tensor cu, kv, pos, slots, left;
-  if (out) {
-    std::tie(cu, kv, pos, slots, left) = *out;
-    for (const at::Tensor* o : {&cu, &kv, &pos, &slots, &left})
-      for (const at::Tensor* i : {&new_lens, &ctx_lens, &n_free})
-        if (o->numel() > 0 && i->numel() > 0 && o->data_ptr() == i->data_ptr()) throw py::value_error("no output may be an input");
-  } else {
-    const at::Tensor buf = make(dev, {2 * B + 2 + 2 * T}, at::kInt);  // 4-byte alignment is all that the step's calls need
-    cu = part(buf, at::kInt, 0, B + 1), kv = part(buf, at::kInt, B + 1, B), pos = part(buf, at::kInt, 2 * B + 1, T);
-    slots = part(buf, at::kInt, 2 * B + 1 + T, T), left = part(buf, at::kInt, 2 * B + 1 + 2 * T, 1);
-  }
-  check(api.plan(ints(dev, "new_lens", new_lens, B), ints(dev, "ctx_lens", ctx_lens, B), B, page_size,
-                 ints(dev, "block_table", block_table, B * width), width, ints(dev, "free_pages", free_pages, n_list), n_list,
-                 ints(dev, "n_free", n_free, 1), T, ints(dev, "cu_new", cu, B + 1), ints(dev, "kv_lens", kv, B),
-                 ints(dev, "positions", pos, T), ints(dev, "slots", slots, T), ints(dev, "n_free_out", left, 1), on.get(dev)),
-        "paged_plan");
+  unlocked("paged_plan", [&] {
+    const int dev = device_of(new_lens, "new_lens");
+    dims("block_table", block_table, 2);
+    const int64_t B = block_table.size(0), width = block_table.size(1), n_list = free_pages.numel();
+    if (T < 0) return BITNET_ERR_SHAPE;
+    if (out) {
+      std::tie(cu, kv, pos, slots, left) = *out;
+      for (const at::Tensor* o : {&cu, &kv, &pos, &slots, &left})
+        for (const at::Tensor* i : {&new_lens, &ctx_lens, &n_free})
+          if (o->numel() > 0 && i->numel() > 0 && o->data_ptr() == i->data_ptr()) throw py::value_error("no output may be an input");
+    } else {
+      const at::Tensor buf = make(dev, {2 * B + 2 + 2 * T}, at::kInt);  // 4-byte alignment is all that the step's calls need
+      cu = part(buf, at::kInt, 0, B + 1), kv = part(buf, at::kInt, B + 1, B), pos = part(buf, at::kInt, 2 * B + 1, T);
+      slots = part(buf, at::kInt, 2 * B + 1 + T, T), left = part(buf, at::kInt, 2 * B + 1 + 2 * T, 1);
+    }
+    return api.plan(ints(dev, "new_lens", new_lens, B), ints(dev, "ctx_lens", ctx_lens, B), B, page_size,
+                   ints(dev, "block_table", block_table, B * width), width, ints(dev, "free_pages", free_pages, n_list), n_list,
+                   ints(dev, "n_free", n_free, 1), T, ints(dev, "cu_new", cu, B + 1), ints(dev, "kv_lens", kv, B),
+                   ints(dev, "positions", pos, T), ints(dev, "slots", slots, T), ints(dev, "n_free_out", left, 1), on.get(dev));
+  });
   return py::make_tuple(cu, kv, pos, slots, left);
 }
 
@@ -171,23 +186,24 @@ at::Tensor rope_paged_append(const at::Tensor& q, const at::Tensor& k, const at:
                              const at::Tensor& slots, double theta, const at::Tensor& k_pages, const at::Tensor& v_pages, Maybe q_rot,
                              const py::object& stream) {
   const OnStream on(stream);
-  const int dev = device_of(q, "q");
-  dims("q", q, 3);
-  dims("k", k, 3);
-  const int64_t T = q.size(0), Hq = q.size(1), d = q.size(2), Hkv = k.size(1), n = T * Hq * d, nk = T * Hkv * d;
-  const at::ScalarType type = q.scalar_type();
-  const bitnet_dtype xt = float_code("q", q);
-  if (k.size(0) != T || k.size(2) != d || v.sizes() != k.sizes()) throw py::value_error("k and v must be [T, Hkv, d]");
-  const Pages pages(dev, k_pages, v_pages, Hkv, d);
-  if (!q_rot) {
-    q_rot = make(dev, {T, Hq, d}, at::kBFloat16);
-  } else if (q_rot->sizes() != q.sizes()) {
-    throw py::value_error("q_rot must have the shape of q");
-  }
-  check(api.rope(arg(dev, "q", q, type, n), arg(dev, "k", k, type, nk), arg(dev, "v", v, type, nk), xt, T, Hq, Hkv, d,
-                 ints(dev, "positions", positions, T), ints(dev, "slots", slots, T), theta, arg(dev, "q_rot", *q_rot, at::kBFloat16, n),
-                 pages.k, pages.v, pages.n, pages.size, on.get(dev)),
-        "rope_paged_append");
+  unlocked("rope_paged_append", [&] {
+    const int dev = device_of(q, "q");
+    dims("q", q, 3);
+    dims("k", k, 3);
+    const int64_t T = q.size(0), Hq = q.size(1), d = q.size(2), Hkv = k.size(1), n = T * Hq * d, nk = T * Hkv * d;
+    const at::ScalarType type = q.scalar_type();
+    const bitnet_dtype xt = float_code("q", q);
+    if (k.size(0) != T || k.size(2) != d || v.sizes() != k.sizes()) throw py::value_error("k and v must be [T, Hkv, d]");
+    const Pages pages(dev, k_pages, v_pages, Hkv, d);
+    if (!q_rot) {
+      q_rot = make(dev, {T, Hq, d}, at::kBFloat16);
+    } else if (q_rot->sizes() != q.sizes()) {
+      throw py::value_error("q_rot must have the shape of q");
+    }
+    return api.rope(arg(dev, "q", q, type, n), arg(dev, "k", k, type, nk), arg(dev, "v", v, type, nk), xt, T, Hq, Hkv, d,
+                   ints(dev, "positions", positions, T), ints(dev, "slots", slots, T), theta, arg(dev, "q_rot", *q_rot, at::kBFloat16, n),
+                   pages.k, pages.v, pages.n, pages.size, on.get(dev));
+  });
   return *q_rot;
 }
 
@@ -195,26 +211,27 @@ at::Tensor attention_paged(const at::Tensor& q_rot, const at::Tensor& k_pages, c
                            const at::Tensor& cu_new, const at::Tensor& kv_lens, int64_t max_new, at::ScalarType out_dtype, Maybe out,
                            Maybe ws, const py::object& stream) {
   const OnStream on(stream);
-  const int dev = device_of(q_rot, "q_rot");
-  dims("q_rot", q_rot, 3);
-  dims("block_table", block_table, 2);
-  dims("k_pages", k_pages, 4);
-  const int64_t T = q_rot.size(0), Hq = q_rot.size(1), d = q_rot.size(2), Hkv = k_pages.size(1), n = T * Hq * d;
-  const int64_t B = block_table.size(0), width = block_table.size(1);
-  const Pages pages(dev, k_pages, v_pages, Hkv, d);
-  if (!out) {
-    out = make(dev, {T, Hq, d}, out_dtype);
-  } else if (out->sizes() != q_rot.sizes()) {
-    throw py::value_error("out must have the shape of q_rot");
-  }
-  const bitnet_dtype ot = float_code("out", *out);
-  if (!ws) ws = make(dev, {std::max<int64_t>((int64_t)api.attention_ws(Hq, Hkv, max_new), 16)}, at::kByte);
-  const int64_t nws = ws->numel();
-  check(api.attention(arg(dev, "q_rot", q_rot, at::kBFloat16, n), pages.k, pages.v, ints(dev, "block_table", block_table, B * width),
-                      ints(dev, "cu_new", cu_new, B + 1), ints(dev, "kv_lens", kv_lens, B), T, B, Hq, Hkv, d, pages.n, pages.size, width,
-                      max_new, arg(dev, "out", *out, out->scalar_type(), n), ot, arg(dev, "ws", *ws, at::kByte, nws), (size_t)nws,
-                      on.get(dev)),
-        "attention_paged");
+  unlocked("attention_paged", [&] {
+    const int dev = device_of(q_rot, "q_rot");
+    dims("q_rot", q_rot, 3);
+    dims("block_table", block_table, 2);
+    dims("k_pages", k_pages, 4);
+    const int64_t T = q_rot.size(0), Hq = q_rot.size(1), d = q_rot.size(2), Hkv = k_pages.size(1), n = T * Hq * d;
+    const int64_t B = block_table.size(0), width = block_table.size(1);
+    const Pages pages(dev, k_pages, v_pages, Hkv, d);
+    if (!out) {
+      out = make(dev, {T, Hq, d}, out_dtype);
+    } else if (out->sizes() != q_rot.sizes()) {
+      throw py::value_error("out must have the shape of q_rot");
+    }
+    const bitnet_dtype ot = float_code("out", *out);
+    if (!ws) ws = make(dev, {std::max<int64_t>((int64_t)api.attention_ws(Hq, Hkv, max_new), 16)}, at::kByte);
+    const int64_t nws = ws->numel();
+    return api.attention(arg(dev, "q_rot", q_rot, at::kBFloat16, n), pages.k, pages.v, ints(dev, "block_table", block_table, B * width),
+                        ints(dev, "cu_new", cu_new, B + 1), ints(dev, "kv_lens", kv_lens, B), T, B, Hq, Hkv, d, pages.n, pages.size, width,
+                        max_new, arg(dev, "out", *out, out->scalar_type(), n), ot, arg(dev, "ws", *ws, at::kByte, nws), (size_t)nws,
+                        on.get(dev));
+  });
   return *out;
 }
 
