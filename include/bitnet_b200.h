@@ -333,7 +333,8 @@ bitnet_status bitnet_attention_decode(const float* q_rot, const void* k_cache, c
  *   r' = x + residual (one fp32 addition, rounded to the residual's type rt)   -> residual_out
  *   (q, s_x, sum_q) = rmsnorm_quant_act(r', gain, eps), bit for bit
  * x [T, K] (xt) is a sublayer's output, residual [T, K] (rt) the stream before it; both types are
- * free.  residual_out may be the residual itself (in place); other overlaps are not allowed.
+ * free.  residual_out may be the residual itself (in place); other overlaps are not allowed (the Python call
+ * refuses them).
  * Errors as bitnet_rmsnorm_quant_act. */
 bitnet_status bitnet_add_rmsnorm_quant_act(const void* x, bitnet_dtype xt, const void* residual, bitnet_dtype rt,
                                            const float* gain, float eps, int64_t T, int64_t K, void* residual_out,
@@ -352,8 +353,9 @@ bitnet_status bitnet_add_rmsnorm_quant_act(const void* x, bitnet_dtype xt, const
  *   slots [T]         its slot (-1 behind the last one)
  * All int32 on the device, 4-byte aligned; n_list is the allocated length of free_pages, n_free
  * [1] how many of its entries are free.  The call takes pages but does not change the list: the
- * caller's new count is n_free_out.  No output may overlap an input (block_table is both).  A calling program returns a
- * finished request's pages by writing them behind the free ones.
+ * caller's new count is n_free_out.  No output may overlap an input or another output, block_table
+ * counting as an output (the Python call refuses it).  A calling program returns a finished
+ * request's pages by writing them behind the free ones.
  * If the free pages do not suffice, n_free_out is negative (how many are missing), the entries
  * and slots without a page are -1, and the step must not be run.  A request with a negative
  * length, or whose tokens exceed width * page_size, gets no pages, its slots are -1 and its kv_len
@@ -371,8 +373,8 @@ bitnet_status bitnet_paged_plan(const int32_t* new_lens, const int32_t* ctx_lens
  * its rotated k and its v go to slot slots[t] of the pages.  q_rot is bf16 [T, Hq, 128] here
  * (nearest even; what the paged attention multiplies).  Tokens with a negative slot are skipped:
  * neither their q_rot nor the cache is written.  A slot of n_pages * page_size or more is skipped
- * too and sets BITNET_ERR_INDEX.  The slots of a call must differ from one another, and no output
- * may overlap an input.  The angle is
+ * too and sets BITNET_ERR_INDEX.  The slots of a call must differ from one another, and no output, the
+ * pages among them, may overlap an input or another output (the Python call refuses it).  The angle is
  * p theta^(-2i/128) reduced to a turn in fp64, its sine and cosine fp32.  Errors: NULL, SHAPE (d != 128, Hq % Hkv,
  * Hq > 1024, page_size, theta <= 0), ALIGN, DTYPE. */
 bitnet_status bitnet_rope_paged_append(const void* q, const void* k, const void* v, bitnet_dtype xt, int64_t T,
@@ -398,7 +400,8 @@ size_t bitnet_attention_paged_workspace_bytes(int64_t Hq, int64_t Hkv, int64_t m
  * a decode step.  Equal calls give equal bits.  A request whose lengths do not
  * fit the call (cu_new descending or beyond T, more than max_new tokens, kv_lens beyond the
  * table) is skipped; a page id outside [0, n_pages) counts as a page of zeros; both set
- * BITNET_ERR_INDEX.  Two calls that share a workspace must not run concurrently.
+ * BITNET_ERR_INDEX.  Two calls that share a workspace must not run concurrently.  A bf16 out may be q_rot
+ * itself; otherwise out and ws may overlap neither an input nor each other (the Python call refuses it).
  * Errors: NULL, SHAPE, ALIGN, DTYPE, WORKSPACE. */
 bitnet_status bitnet_attention_paged(const void* q_rot, const void* k_pages, const void* v_pages,
                                      const int32_t* block_table, const int32_t* cu_new, const int32_t* kv_lens,

@@ -10,6 +10,7 @@
 #include <dlfcn.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <initializer_list>
 #include <optional>
 #include <string>
 
@@ -89,6 +90,24 @@ at::Tensor make(int dev, at::IntArrayRef size, at::ScalarType type) {
   return at::Tensor(at::detail::empty_cuda(size, type, at::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt));
 }
 
+// The bytes of contiguous tensors, and the refusal of overlaps that would let a kernel read what another part of it
+// has already written.
+struct Bytes {
+  uintptr_t from, to;
+  Bytes(const at::Tensor& t) : from(t.numel() ? reinterpret_cast<uintptr_t>(t.data_ptr()) : 0), to(t.numel() ? from + t.nbytes() : 0) {}
+  bool meets(const Bytes& o) const { return from < o.to && o.from < to; }
+  bool is(const Bytes& o) const { return from == o.from && to == o.to; }
+};
+// No output overlaps an input or another output.
+void apart(std::initializer_list<Bytes> outs, std::initializer_list<Bytes> ins) {
+  for (const Bytes* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Bytes& i : ins)
+      if (o->meets(i)) throw py::value_error("an output must not overlap an input");
+    for (const Bytes* p = outs.begin(); p != o; ++p)
+      if (o->meets(*p)) throw py::value_error("outputs must not overlap one another");
+  }
+}
+
 // `n` entries of 4 bytes of `buf` from entry `at` on, as a tensor of their own (an allocation takes 0.7 us, this 0.2).
 at::Tensor part(const at::Tensor& buf, at::ScalarType type, int64_t at, int64_t n) {
   at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buf.storage()), buf.key_set(), c10::scalarTypeToTypeMeta(type));
@@ -121,13 +140,18 @@ py::tuple add_rmsnorm_quant_act(const at::Tensor& x, const at::Tensor& residual,
     const int64_t T = x.size(0), K = x.size(1), n = T * K;
     const bitnet_dtype xt = float_code("x", x), rt = float_code("residual", residual);
     if (residual.sizes() != x.sizes()) throw py::value_error("residual must have the shape of x");
+    const at::Tensor& g = gain ? *gain : residual;
     if (!residual_out) {
       residual_out = make(dev, {T, K}, residual.scalar_type());
-    } else if (residual_out->sizes() != x.sizes()) {
-      throw py::value_error("residual_out must have the shape of x");
+    } else {
+      if (residual_out->sizes() != x.sizes()) throw py::value_error("residual_out must have the shape of x");
+      apart({*residual_out}, {x});
+      if (!Bytes(*residual_out).is(residual)) apart({*residual_out}, {residual, g});  // in place, or elsewhere
     }
     if (out) {
       std::tie(q, s, sq) = *out;
+      apart({q, s, sq, *residual_out}, {x});
+      apart({q, s, sq}, {residual, g});
     } else {
       const int64_t second = (T + 3) / 4 * 4;  // 16-byte aligned
       const at::Tensor rows = make(dev, {second + T}, at::kInt);
@@ -155,10 +179,9 @@ py::tuple paged_plan(const at::Tensor& new_lens, const at::Tensor& ctx_lens, con
     if (T < 0) return BITNET_ERR_SHAPE;
     if (out) {
       std::tie(cu, kv, pos, slots, left) = *out;
-      for (const at::Tensor* o : {&cu, &kv, &pos, &slots, &left})
-        for (const at::Tensor* i : {&new_lens, &ctx_lens, &n_free})
-          if (o->numel() > 0 && i->numel() > 0 && o->data_ptr() == i->data_ptr()) throw py::value_error("no output may be an input");
+      apart({cu, kv, pos, slots, left, block_table}, {new_lens, ctx_lens, free_pages, n_free});
     } else {
+      apart({block_table}, {new_lens, ctx_lens, free_pages, n_free});
       const at::Tensor buf = make(dev, {2 * B + 2 + 2 * T}, at::kInt);  // 4-byte alignment is all that the step's calls need
       cu = part(buf, at::kInt, 0, B + 1), kv = part(buf, at::kInt, B + 1, B), pos = part(buf, at::kInt, 2 * B + 1, T);
       slots = part(buf, at::kInt, 2 * B + 1 + T, T), left = part(buf, at::kInt, 2 * B + 1 + 2 * T, 1);
@@ -197,8 +220,10 @@ at::Tensor rope_paged_append(const at::Tensor& q, const at::Tensor& k, const at:
     const Pages pages(dev, k_pages, v_pages, Hkv, d);
     if (!q_rot) {
       q_rot = make(dev, {T, Hq, d}, at::kBFloat16);
-    } else if (q_rot->sizes() != q.sizes()) {
-      throw py::value_error("q_rot must have the shape of q");
+      apart({k_pages, v_pages}, {q, k, v, positions, slots});
+    } else {
+      if (q_rot->sizes() != q.sizes()) throw py::value_error("q_rot must have the shape of q");
+      apart({*q_rot, k_pages, v_pages}, {q, k, v, positions, slots});
     }
     return api.rope(arg(dev, "q", q, type, n), arg(dev, "k", k, type, nk), arg(dev, "v", v, type, nk), xt, T, Hq, Hkv, d,
                    ints(dev, "positions", positions, T), ints(dev, "slots", slots, T), theta, arg(dev, "q_rot", *q_rot, at::kBFloat16, n),
@@ -221,11 +246,18 @@ at::Tensor attention_paged(const at::Tensor& q_rot, const at::Tensor& k_pages, c
     const Pages pages(dev, k_pages, v_pages, Hkv, d);
     if (!out) {
       out = make(dev, {T, Hq, d}, out_dtype);
-    } else if (out->sizes() != q_rot.sizes()) {
-      throw py::value_error("out must have the shape of q_rot");
+    } else {
+      if (out->sizes() != q_rot.sizes()) throw py::value_error("out must have the shape of q_rot");
+      apart({*out}, {k_pages, v_pages, block_table, cu_new, kv_lens});
+      if (!Bytes(*out).is(q_rot)) apart({*out}, {q_rot});  // in place, or elsewhere
     }
     const bitnet_dtype ot = float_code("out", *out);
-    if (!ws) ws = make(dev, {std::max<int64_t>((int64_t)api.attention_ws(Hq, Hkv, max_new), 16)}, at::kByte);
+    if (!ws) {
+      ws = make(dev, {std::max<int64_t>((int64_t)api.attention_ws(Hq, Hkv, max_new), 16)}, at::kByte);
+    } else {
+      apart({*ws, *out}, {k_pages, v_pages, block_table, cu_new, kv_lens});
+      apart({*ws}, {q_rot});
+    }
     const int64_t nws = ws->numel();
     return api.attention(arg(dev, "q_rot", q_rot, at::kBFloat16, n), pages.k, pages.v, ints(dev, "block_table", block_table, B * width),
                         ints(dev, "cu_new", cu_new, B + 1), ints(dev, "kv_lens", kv_lens, B), T, B, Hq, Hkv, d, pages.n, pages.size, width,
