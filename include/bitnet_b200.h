@@ -399,9 +399,10 @@ size_t bitnet_attention_paged_workspace_bytes(int64_t Hq, int64_t Hkv, int64_t m
  * bf16 (2^-8, below the output's own rounding).  So fp32 outputs are as precise in a step that holds a chunk as in
  * a decode step.  Equal calls give equal bits.  A request whose lengths do not
  * fit the call (cu_new descending or beyond T, more than max_new tokens, kv_lens beyond the
- * table) is skipped; a page id outside [0, n_pages) counts as a page of zeros; both set
+ * table) is skipped (so with max_new = 0 every request that has tokens); a page id outside [0, n_pages) counts as a page of zeros; both set
  * BITNET_ERR_INDEX.  Two calls that share a workspace must not run concurrently.  A bf16 out may be q_rot
  * itself; otherwise out and ws may overlap neither an input nor each other (the Python call refuses it).
+ * T = 0, B = 0, and max_new = 0 with q_rot NULL, return without a launch.
  * Errors: NULL, SHAPE, ALIGN, DTYPE, WORKSPACE. */
 bitnet_status bitnet_attention_paged(const void* q_rot, const void* k_pages, const void* v_pages,
                                      const int32_t* block_table, const int32_t* cu_new, const int32_t* kv_lens,

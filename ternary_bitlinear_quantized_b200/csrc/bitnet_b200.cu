@@ -1371,7 +1371,8 @@ bitnet_status bitnet_attention_paged(const void* q_rot, const void* k_pages, con
       Hq % Hkv || d != PG_D || log2P < 0 || n_pages <= 0 || n_pages * page_size > 0x7FFFFFFFll || width <= 0 ||
       width * page_size > BITNET_MAX_KV_ROWS || max_new < 0)
     return BITNET_ERR_SHAPE;
-  if (T == 0 || B == 0 || max_new == 0) return BITNET_OK;
+  if (T == 0 || B == 0) return BITNET_OK;
+  if (max_new == 0 && !q_rot) return BITNET_OK;  // no rows are meant and none given; with rows the kernel flags requests that have some
   if (!q_rot || !k_pages || !v_pages || !block_table || !cu_new || !kv_lens || !out) return BITNET_ERR_NULL;
   if (!ws || ws_bytes < bitnet_attention_paged_workspace_bytes(Hq, Hkv, max_new)) return BITNET_ERR_WORKSPACE;
   for (const void* p : {q_rot, k_pages, v_pages, (const void*)out, (const void*)ws})

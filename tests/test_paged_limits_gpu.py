@@ -170,3 +170,14 @@ def test_attention_refuses_outputs_that_overlap_but_for_q_itself(new):
         q = b.q.clone()
         got = tb.attention_paged(q, *args, out=q, ws=ws)
         assert got.data_ptr() == q.data_ptr() and torch.equal(got[: 2 * new], want[: 2 * new]) and torch.equal(got[2 * new:], b.q[2 * new:])
+
+
+def test_a_max_new_of_zero_is_too_small_for_requests_with_tokens():
+    """As with any max_new that a request exceeds: the request is skipped and flagged."""
+    b = Batch([1, 0, 1], [40, 7, 90], 8, 2, 16)
+    out = torch.full(b.q.shape, 77.0, dtype=torch.bfloat16, device=DEV)
+    tb.attention_paged(b.q, b.kp, b.vp, b.table, b.cu, b.kv, 0, out=out)
+    assert tb.device_status() == 8 and (out == 77.0).all()
+    b.cu.zero_()  # no request has tokens: nothing to flag
+    tb.attention_paged(b.q, b.kp, b.vp, b.table, b.cu, b.kv, 0, out=out)
+    assert tb.device_status() == 0 and (out == 77.0).all()
