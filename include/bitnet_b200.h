@@ -376,7 +376,7 @@ bitnet_status bitnet_paged_plan(const int32_t* new_lens, const int32_t* ctx_lens
  * too and sets BITNET_ERR_INDEX.  The slots of a call must differ from one another, and no output, the
  * pages among them, may overlap an input or another output (the Python call refuses it).  The angle is
  * p theta^(-2i/128) reduced to a turn in fp64, its sine and cosine fp32.  Errors: NULL, SHAPE (d != 128, Hq % Hkv,
- * Hq > 1024, page_size, theta <= 0), ALIGN, DTYPE. */
+ * Hq > 1024, page_size, theta not in [1, inf)), ALIGN, DTYPE. */
 bitnet_status bitnet_rope_paged_append(const void* q, const void* k, const void* v, bitnet_dtype xt, int64_t T,
                                        int64_t Hq, int64_t Hkv, int64_t d, const int32_t* positions,
                                        const int32_t* slots, double theta, void* q_rot, void* k_pages, void* v_pages,

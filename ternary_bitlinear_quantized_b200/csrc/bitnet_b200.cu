@@ -1301,7 +1301,8 @@ bitnet_status bitnet_rope_paged_append(const void* q, const void* k, const void*
                                        int64_t n_pages, int64_t page_size, bitnet_stream stream) {
   if (xt != BITNET_BF16 && xt != BITNET_F32) return BITNET_ERR_DTYPE;
   if (T < 0 || T > BITNET_MAX_STEP_TOKENS || Hq <= 0 || Hkv <= 0 || Hq > 1024 || Hq % Hkv || d != PG_D ||
-      page_log2(page_size) < 0 || n_pages <= 0 || n_pages * page_size > 0x7FFFFFFFll || !(theta > 0.0))
+      page_log2(page_size) < 0 || n_pages <= 0 || n_pages * page_size > 0x7FFFFFFFll || !(theta >= 1.0) ||
+      std::isinf(theta))  // below 1 the angles outgrow the positions, and with them the error of their reduction
     return BITNET_ERR_SHAPE;
   if (T == 0) return BITNET_OK;
   if (!q || !k || !v || !positions || !slots || !q_rot || !k_pages || !v_pages) return BITNET_ERR_NULL;

@@ -1,0 +1,36 @@
+"""Edges of the paged serving step that need no GPU: sizes whose products pass 64 bits, angles that the rotary call
+does not take, the polynomial exponential of the attention of chunks, and what the built binding was built for."""
+from __future__ import annotations
+
+import ctypes
+
+import numpy as np
+import pytest
+
+import ternary_bitlinear_quantized_b200 as tb
+from ternary_bitlinear_quantized_b200 import build as tbuild
+
+P16 = ctypes.c_void_p(16)  # never dereferenced: every call fails its checks first
+ROPE = dict(q=P16, k=P16, v=P16, xt=0, T=1, Hq=4, Hkv=2, d=128, pos=P16, slots=P16, theta=1e4, qr=P16, kp=P16, vp=P16, n=3,
+            P=16, st=None)
+PLAN = dict(new=P16, ctx=P16, B=2, P=16, tab=P16, width=4, free=P16, n_list=8, n_free=P16, T=3, cu=P16, kv=P16, pos=P16,
+            slots=P16, out=P16, st=None)
+ATTENTION = dict(q=P16, kp=P16, vp=P16, tab=P16, cu=P16, kv=P16, T=1, B=1, Hq=4, Hkv=2, d=128, n=3, P=16, width=4, max_new=1,
+                 out=P16, ot=0, ws=P16, ws_bytes=1 << 40, st=None)
+
+
+@pytest.fixture(scope="module")
+def L():
+    tbuild.build()
+    return tb.lib()
+
+
+def _call(fn, args, **change):
+    return fn(*dict(args, **change).values())
+
+
+@pytest.mark.parametrize("theta", [0.999, 1e-6, 1e-300, -1.0, float("inf"), float("nan")])
+def test_rope_refuses_angles_that_outgrow_the_positions(L, theta):
+    """Below theta = 1 the pairs turn by more than their position, and the fp64 reduction to one turn loses its accuracy."""
+    assert _call(L.bitnet_rope_paged_append, ROPE, theta=theta) == 2
+    assert _call(L.bitnet_rope_paged_append, ROPE, theta=1.0, q=None) == 1  # 1 itself passes that check: the next one answers
