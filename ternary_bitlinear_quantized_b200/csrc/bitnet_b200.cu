@@ -1278,7 +1278,7 @@ bitnet_status bitnet_paged_plan(const int32_t* new_lens, const int32_t* ctx_lens
                                 const int32_t* n_free, int64_t T, int32_t* cu_new, int32_t* kv_lens,
                                 int32_t* positions, int32_t* slots, int32_t* n_free_out, bitnet_stream stream) {
   if (B < 0 || B > BITNET_MAX_REQUESTS || T < 0 || T > BITNET_MAX_STEP_TOKENS || page_log2(page_size) < 0 ||
-      width <= 0 || width * page_size > BITNET_MAX_KV_ROWS || n_list < 0 || n_list > 0x7FFFFFFFll)
+      width <= 0 || width > BITNET_MAX_KV_ROWS / page_size || n_list < 0 || n_list > 0x7FFFFFFFll)
     return BITNET_ERR_SHAPE;
   if (!cu_new || !n_free || !n_free_out || (B > 0 && (!new_lens || !ctx_lens || !block_table || !kv_lens)) ||
       (n_list > 0 && !free_pages) || (T > 0 && (!positions || !slots)))
@@ -1301,7 +1301,7 @@ bitnet_status bitnet_rope_paged_append(const void* q, const void* k, const void*
                                        int64_t n_pages, int64_t page_size, bitnet_stream stream) {
   if (xt != BITNET_BF16 && xt != BITNET_F32) return BITNET_ERR_DTYPE;
   if (T < 0 || T > BITNET_MAX_STEP_TOKENS || Hq <= 0 || Hkv <= 0 || Hq > 1024 || Hq % Hkv || d != PG_D ||
-      page_log2(page_size) < 0 || n_pages <= 0 || n_pages * page_size > 0x7FFFFFFFll || !(theta >= 1.0) ||
+      page_log2(page_size) < 0 || n_pages <= 0 || n_pages > 0x7FFFFFFFll / page_size || !(theta >= 1.0) ||
       std::isinf(theta))  // below 1 the angles outgrow the positions, and with them the error of their reduction
     return BITNET_ERR_SHAPE;
   if (T == 0) return BITNET_OK;
@@ -1369,8 +1369,8 @@ bitnet_status bitnet_attention_paged(const void* q_rot, const void* k_pages, con
   if (ot != BITNET_BF16 && ot != BITNET_F32) return BITNET_ERR_DTYPE;
   const int log2P = page_log2(page_size);
   if (T < 0 || T > BITNET_MAX_STEP_TOKENS || B < 0 || B > BITNET_MAX_REQUESTS || Hq <= 0 || Hkv <= 0 || Hq > 1024 ||
-      Hq % Hkv || d != PG_D || log2P < 0 || n_pages <= 0 || n_pages * page_size > 0x7FFFFFFFll || width <= 0 ||
-      width * page_size > BITNET_MAX_KV_ROWS || max_new < 0)
+      Hq % Hkv || d != PG_D || log2P < 0 || n_pages <= 0 || n_pages > 0x7FFFFFFFll / page_size || width <= 0 ||
+      width > BITNET_MAX_KV_ROWS / page_size || max_new < 0)
     return BITNET_ERR_SHAPE;
   if (T == 0 || B == 0) return BITNET_OK;
   if (max_new == 0 && !q_rot) return BITNET_OK;  // no rows are meant and none given; with rows the kernel flags requests that have some

@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const int* __restri
 // g_i = theta^(-2i/128) / (2 pi) in fp64, so a is p g_i turns: its whole turns are dropped in
 // fp64 (p g_i - rint(p g_i) is exact) and sine and cosine of pi times the rest, |rest| <= 1,
 // taken in fp32.  theta >= 1, so |p g_i| <= |p| / (2 pi) < 2^29, and the fp64 product is off by at most
-// 2^-23 turns there (g_i's rounding and its own, 2^-53 of it each) and by 2^-37 at positions below 2^16.  The rotation is fp32, one rounding an operation; q_rot and the
-// cache are bf16 (nearest even).
+// 2^-23 turns there (g_i's rounding and its own, 2^-53 of it each) and by 2^-37 at positions below 2^16.
+// The rotation is fp32, one rounding an operation; q_rot and the cache are bf16 (nearest even).
 //
 // Bound by HBM: each value is read and written once.  A CTA takes TOKENS tokens: their 64
 // angles each are made once and shared by all heads (a sine and cosine per head would cost more

@@ -34,3 +34,21 @@ def test_rope_refuses_angles_that_outgrow_the_positions(L, theta):
     """Below theta = 1 the pairs turn by more than their position, and the fp64 reduction to one turn loses its accuracy."""
     assert _call(L.bitnet_rope_paged_append, ROPE, theta=theta) == 2
     assert _call(L.bitnet_rope_paged_append, ROPE, theta=1.0, q=None) == 1  # 1 itself passes that check: the next one answers
+
+
+@pytest.mark.parametrize("extra", [0, 5, 1])
+@pytest.mark.parametrize("P", [16, 256])
+def test_sizes_whose_products_pass_64_bits_are_refused(L, P, extra):
+    """n_pages page_size and width page_size of 2^64 and little more, which are little numbers in 64 bits."""
+    big = (1 << 64) // P // 2 * 2 + extra
+    for n in (big, big // 2, big // 16, (1 << 31) // P + extra):
+        n = min(n, (1 << 63) - 1)
+        assert _call(L.bitnet_rope_paged_append, ROPE, P=P, n=n) == 2
+        assert _call(L.bitnet_attention_paged, ATTENTION, P=P, n=n) == 2
+        assert _call(L.bitnet_attention_paged, ATTENTION, P=P, width=n) == 2
+        assert _call(L.bitnet_paged_plan, PLAN, P=P, width=n) == 2
+    # the largest there are pass that check: the next one answers
+    n = 0x7FFFFFFF // P
+    assert _call(L.bitnet_rope_paged_append, ROPE, P=P, n=n, q=None) == 1
+    assert _call(L.bitnet_attention_paged, ATTENTION, P=P, n=n, width=(1 << 30) // P, q=None) == 1
+    assert _call(L.bitnet_paged_plan, PLAN, P=P, width=(1 << 30) // P, cu=None) == 1
