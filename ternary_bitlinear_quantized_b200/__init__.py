@@ -420,9 +420,10 @@ _native = None
 def _load_serving():
     global _native
     if _native is None:
-        path = os.path.join(_HERE, "_serving.so")
-        if not os.path.exists(path):
-            raise ImportError(f"{path} is missing: build it with `python -m ternary_bitlinear_quantized_b200.build`")
+        from . import build
+        if not build.binding_fits():
+            raise ImportError(f"{build.BINDING} is missing or not {build.built_for()[1:-1]}: "
+                              "build it with `python -m ternary_bitlinear_quantized_b200.build`")
         handle = lib()._handle
         from . import _serving as native
         native.bind(handle, BitnetError)

@@ -10,6 +10,9 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -36,19 +39,32 @@ def build(verbose: bool = False, force: bool = False) -> str:
                                   "-shared", "-cudart", "static", *include, os.path.join(CSRC, "bitnet_b200.cu"),
                                   *(["-Xptxas=-v"] if verbose else [])], verbose, force)
     src = os.path.join(CSRC, "serving_binding.cpp")
-    if force or _stale(BINDING, [src, hdr]):  # the import of torch takes longer than the check
-        import sysconfig
-
-        import torch
+    other = not binding_fits()  # built for another torch or Python
+    if force or other or _stale(BINDING, [src, hdr]):
         root = os.path.dirname(torch.__file__)
         cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
         dirs = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], cuda]
         _run(BINDING, [src, hdr], [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
                                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                                   f'-DSERVING_BUILT_FOR="{built_for()}"',
                                    *[f"-I{d}" for d in dirs], src, "-L" + os.path.join(root, "lib"), "-ltorch_python",
-                                   "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-ltorch"], verbose, force)
+                                   "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-ltorch"], verbose, force or other)
     return LIB
+
+
+def built_for() -> str:
+    """What the native binding depends on beside its source: Python's ABI and torch's."""
+    return f"[built for {sysconfig.get_config_var('SOABI')}, torch {torch.__version__}]"
+
+
+def binding_fits() -> bool:
+    """Whether the built binding is there and is for this Python and torch.  The file is read, not loaded: one that does not
+    fit may not survive its import."""
+    if not os.path.exists(BINDING):
+        return False
+    with open(BINDING, "rb") as f:
+        return built_for().encode() in f.read()
 
 
 def _stale(out: str, srcs: list[str]) -> bool:

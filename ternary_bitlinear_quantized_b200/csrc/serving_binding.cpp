@@ -270,6 +270,7 @@ at::Tensor attention_paged(const at::Tensor& q_rot, const at::Tensor& k_pages, c
 }  // namespace
 
 PYBIND11_MODULE(_serving, m) {
+  m.attr("built_for") = SERVING_BUILT_FOR;  // looked for in the file before it is loaded
   m.def("bind", &bind);
   m.def("add_rmsnorm_quant_act", &add_rmsnorm_quant_act);
   m.def("paged_plan", &paged_plan);

@@ -52,3 +52,21 @@ def test_sizes_whose_products_pass_64_bits_are_refused(L, P, extra):
     assert _call(L.bitnet_rope_paged_append, ROPE, P=P, n=n, q=None) == 1
     assert _call(L.bitnet_attention_paged, ATTENTION, P=P, n=n, width=(1 << 30) // P, q=None) == 1
     assert _call(L.bitnet_paged_plan, PLAN, P=P, width=(1 << 30) // P, cu=None) == 1
+
+
+def test_the_binding_is_built_again_for_another_torch_or_python(L, monkeypatch):
+    """A binary for another ABI is neither kept by the build nor loaded."""
+    assert tbuild.binding_fits() and tb._load_serving().built_for == tbuild.built_for()
+    runs = []
+    monkeypatch.setattr(tbuild, "_run", lambda out, srcs, cmd, verbose, force: runs.append((out, cmd, force)))
+    tbuild.build()
+    assert not any(force for _, _, force in runs) and tbuild.BINDING not in [out for out, _, _ in runs]
+    monkeypatch.setattr(tbuild.torch, "__version__", tbuild.torch.__version__ + ".1")
+    assert not tbuild.binding_fits()
+    runs.clear()
+    tbuild.build()
+    out, cmd, force = runs[-1]
+    assert out == tbuild.BINDING and force and any(tbuild.built_for() in c for c in cmd)
+    monkeypatch.setattr(tb, "_native", None)
+    with pytest.raises(ImportError, match="build it with"):
+        tb._load_serving()
