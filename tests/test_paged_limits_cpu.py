@@ -70,3 +70,34 @@ def test_the_binding_is_built_again_for_another_torch_or_python(L, monkeypatch):
     monkeypatch.setattr(tb, "_native", None)
     with pytest.raises(ImportError, match="build it with"):
         tb._load_serving()
+
+
+def _exp2_pair(z):
+    """exp2_pair of attn_chunk.cuh: the same fp32 steps.  fma: the exact product and sum in fp64, rounded once to fp32 but
+    for double rounding (fp64 holds the product of two fp32 exactly; a tie that fp64 makes of a sum is off by 2^-53 of it)."""
+    f32 = np.float32
+    fma = lambda a, b, c: (a.astype(np.float64) * np.float64(b) + np.float64(c)).astype(f32)  # noqa: E731
+    z = np.maximum(z.astype(f32), f32(-127))
+    t = (z + f32(12582912.0)).astype(f32)
+    n = (t + f32(-12582912.0)).astype(f32)
+    f = (z - n).astype(f32)  # exact: n is the integer next to z
+    p = np.full_like(z, f32(0.001326472032815218))
+    for c in (0.009671512991189957, 0.05550733581185341, 0.24022242426872253, 0.6931470036506653, 1.0):
+        p = fma(p, f, f32(c))
+    return (p.view(np.uint32) + (t.view(np.uint32) << np.uint32(23))).view(f32)
+
+
+def test_polynomial_exponential():
+    """Its documented error: 2^-23.1 by the coefficients, 2^-22.4 as evaluated in fp32; powers of two exact; weights of scores
+    far below the maximum, and of masked ones, zero or below the smallest normal number."""
+    f = np.linspace(-0.5, 0.5, 400001)
+    c = np.float32([0.001326472032815218, 0.009671512991189957, 0.05550733581185341, 0.24022242426872253, 0.6931470036506653, 1.0])
+    assert np.abs(np.polyval(c.astype(np.float64), f) / 2.0 ** f - 1).max() <= 2.0 ** -23.1
+    rng = np.random.default_rng(0)
+    z = np.concatenate([np.linspace(-125.4, 8.0, 1500001), rng.uniform(-1, 1, 500000), np.arange(-125, 9) + 0.5,
+                        np.arange(-125, 9) - 0.5]).astype(np.float32)
+    assert np.abs(_exp2_pair(z).astype(np.float64) / 2.0 ** z.astype(np.float64) - 1).max() <= 2.0 ** -22.4
+    whole = np.arange(-126, 9).astype(np.float32)
+    assert np.array_equal(_exp2_pair(whole).astype(np.float64), 2.0 ** whole.astype(np.float64))
+    low = _exp2_pair(np.concatenate([np.float32([-np.inf, -1e30, -127.0]), np.linspace(-200, -126.6, 1000).astype(np.float32)]))
+    assert not low[:3].any() and (low >= 0).all() and (low < 2.0 ** -126).all()
