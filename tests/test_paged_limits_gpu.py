@@ -181,3 +181,36 @@ def test_a_max_new_of_zero_is_too_small_for_requests_with_tokens():
     b.cu.zero_()  # no request has tokens: nothing to flag
     tb.attention_paged(b.q, b.kp, b.vp, b.table, b.cu, b.kv, 0, out=out)
     assert tb.device_status() == 0 and (out == 77.0).all()
+
+
+# The kernel for many rows gives each request 32, 16, .. 1 of its 384 threads (up to 12, 24, .. 384 requests), and takes more
+# requests in rounds: a chunk or two among many requests of one token or none, at the start, in the middle and at the end.
+@pytest.mark.parametrize("B", [12, 13, 25, 60, 97, 200, 384, 385, 800, 1300])
+@pytest.mark.parametrize("at", ["start", "middle", "end", "both"])
+def test_chunks_among_many_requests(B, at):
+    new, kv = [0 if i % 5 == 2 else 1 for i in range(B)], [(37 * i) % 150 + 1 for i in range(B)]
+    for i, n, k in {"start": [(0, 70, 200)], "middle": [(B // 2, 45, 45), (B // 2 + 1, 33, 20)], "end": [(B - 1, 100, 390)],
+                    "both": [(0, 40, 41), (B - 1, 64, 700)]}[at]:
+        new[i], kv[i] = n, k
+    b = Batch(new, kv, 8, 2, 16, seed=B, pad=2)
+    out = torch.full(b.q.shape, 77.0, dtype=torch.bfloat16, device=DEV)
+    tb.attention_paged(b.q, b.kp, b.vp, b.table, b.cu, b.kv, b.max_new, out=out)
+    assert tb.device_status() == 0 and (out[sum(new):] == 77.0).all()
+    check_attention(b, out)
+    assert torch.equal(out[: sum(new)], tb.attention_paged(b.q, b.kp, b.vp, b.table, b.cu, b.kv, b.max_new)[: sum(new)])
+
+
+@pytest.mark.parametrize("B", [385, 2000])
+def test_many_requests_some_of_which_do_not_fit(B):
+    new, kv = [1] * B, [(61 * i) % 90 + 1 for i in range(B)]
+    new[B // 2], kv[B // 2] = 50, 60
+    b = Batch(new, kv, 4, 2, 16, seed=1)
+    skip = (0, 7, B // 2 + 1, B - 1)
+    for i in skip:
+        b.kv[i] = b.width * 16 + 1
+    out = torch.full(b.q.shape, 77.0, dtype=torch.bfloat16, device=DEV)
+    tb.attention_paged(b.q, b.kp, b.vp, b.table, b.cu, b.kv, b.max_new, out=out)
+    assert tb.device_status() == 8
+    check_attention(b, out, skip=skip)
+    for i in skip:
+        assert (out[sum(new[:i]): sum(new[: i + 1])] == 77.0).all()
