@@ -1346,8 +1346,9 @@ static bool make_map_heads(CUtensorMap* m, const void* base, int64_t d1, int64_t
 // Which kernel a call takes: up to PAGED_FEW_ROWS query rows per request and key/value head the
 // mma.sync one, which reads the cache once per 16 rows, above them the tcgen05 one, which takes
 // the same time for 1 to 128 rows.  16 requests behind 4096 rows, 8 heads: 16 rows 53 against 60 us,
-// 32 rows 70 against 60 us, 48 rows 134 against 61 us; one request behind 8192 rows, 5 heads, 32 rows:
-// 18 against 24 us.
+// 32 rows 73 against 60 us, 48 rows 134 against 60 us; one request behind 8192 rows, 5 heads, 32 rows:
+// 18 against 24 us.  So at 17 to 32 rows the limit is right for one request and costs a batch a fifth: the
+// rule looks at the rows alone, which fix the workspace and the weights' precision before a batch is known.
 constexpr int64_t PAGED_FEW_ROWS = 32;
 static bool paged_few(int64_t G, int64_t max_new) { return max_new <= PAGED_FEW_ROWS / G; }
 static int paged_ctas(bool few) { return (few ? 2 : 1) * device_sm_count(); }

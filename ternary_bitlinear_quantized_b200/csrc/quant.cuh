@@ -562,7 +562,8 @@ __global__ void __launch_bounds__(QW_THREADS) k_rmsnorm_quant_warps(const TIn* _
 // (as in k_rmsnorm_quant_long), and additions and products are done two at a time.
 // T = K = 8192, bf16: 150 us with 64 values a thread and one load, add and store after the other,
 // 94 us with the loads first and 32 values, 82 us with fewer instructions, 80.4 us (5.8 TB/s) with the
-// warp-wide reduction instruction (K = 12288: 75 instead of 89 us).
+// warp-wide reduction instruction (K = 12288: 75 instead of 89 us).  These are repeated calls over the same
+// buffers, part of whose writes stay in L2; over inputs of several seeds in turn 81 to 90 us (5.2 to 5.8 TB/s).
 // Values behind the row are 0: their terms and codes are those of 0 and cancel with the offsets.
 // Pairs of fp32 in one 64-bit register, one instruction for both.
 BN_DEV uint64_t pair(float lo, float hi) {
